@@ -227,7 +227,7 @@ def prepare(case, seed):
         st["kept"] = torch.empty(B, K, case["budget"], dtype=torch.int32, device="cuda")
     if own:
         from shifted_window_attention_pad_b200 import binding as sb
-        more = {k: case[k] for k in ("window", "sinks", "recent", "budget") if k in case}
+        more = {k: case[k] for k in ("window", "sinks", "recent", "budget", "weights") if k in case}
         kv_stride = 2 * K * hd if case["op"] == "append" else 0
         st["desc"] = sb.make_cache_desc(B, H, hd, ps, pages, width, case["dtype"], kv_heads=K,
                                         kv_stride=kv_stride, **more)
