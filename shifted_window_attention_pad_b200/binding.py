@@ -1,6 +1,6 @@
 """Python binding of libswinwattn.so: argument marshalling only.
 
-Same names as the C ABI in include/swin_wattn.h. Every step of the
+Same names as the C ABI in include/swin_wattn.h and include/swin_seqattn.h. Every step of the
 computation runs in the library's CUDA kernels; this module checks tensor
 devices, dtypes and contiguity, passes raw pointers and the current CUDA
 stream, and turns negative status codes into exceptions. torch is used for
@@ -24,12 +24,16 @@ SWIN_FLAG_FORCE_GENERIC = 1
 SWIN_FLAG_TEST_TIMEOUT = 2
 SWIN_FLAG_FORCE_TILED = 4
 SWIN_FLAG_DBIAS_SUMS = 8
+SWIN_FLAG_KV_WEIGHTS = 256
 
 EXPORTED = ("swin_wattn_path", "swin_wattn_workspace_size", "swin_wattn_fwd", "swin_wattn_bwd",
             "swin_wattn_bwd_noalloc", "swin_wattn_index_map", "swin_wattn_layout_map",
             "swin_wattn_dbias_sums", "swin_wattn_dbias_finish", "swin_wattn_fwd_band",
             "swin_wattn_bwd_band", "swin_wattn_poll_status",
-            "swin_wattn_strerror", "swin_wattn_launch_count")
+            "swin_wattn_strerror", "swin_wattn_launch_count",
+            "swin_seqattn_path", "swin_seqattn_workspace_size", "swin_seqattn_fwd",
+            "swin_seqattn_bwd", "swin_kvcache_workspace_size", "swin_kvcache_append",
+            "swin_kvcache_decode", "swin_kvcache_evict")
 SWIN_NOALLOC_SCRATCH_BYTES = 1 << 20   # include/swin_wattn.h
 
 
@@ -46,6 +50,21 @@ class SwinWattnHalo(ctypes.Structure):
                 ("v", ctypes.c_void_p), ("dout", ctypes.c_void_p), ("out", ctypes.c_void_p),
                 ("lse", ctypes.c_void_p), ("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p),
                 ("dv", ctypes.c_void_p)]
+
+
+class SwinSeqattnDesc(ctypes.Structure):
+    """Attention along a token sequence (include/swin_seqattn.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("B", "S", "heads", "kv_heads", "head_dim", "window", "sinks", "dtype", "flags",
+                 "q_stride", "kv_stride")]
+
+
+class SwinKvcacheDesc(ctypes.Structure):
+    """Paged key-value cache (include/swin_seqattn.h)."""
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("B", "heads", "kv_heads", "head_dim", "page_size", "num_pages", "max_pages",
+                 "window", "sinks", "recent", "budget", "dtype", "flags", "q_stride",
+                 "kv_stride")]
 
 
 class SwinWattnError(RuntimeError):
@@ -89,6 +108,17 @@ def lib():
                   "swin_wattn_bwd", "swin_wattn_bwd_noalloc", "swin_wattn_index_map",
                   "swin_wattn_layout_map", "swin_wattn_dbias_sums", "swin_wattn_dbias_finish",
                   "swin_wattn_fwd_band", "swin_wattn_bwd_band", "swin_wattn_poll_status"):
+            getattr(L, f).restype = ctypes.c_int
+        Q, C, Z = ctypes.POINTER(SwinSeqattnDesc), ctypes.POINTER(SwinKvcacheDesc), ctypes.c_size_t
+        for f, a in (("swin_seqattn_path", [Q]),
+                     ("swin_seqattn_workspace_size", [Q, ctypes.POINTER(Z)]),
+                     ("swin_seqattn_fwd", [Q] + [P] * 7 + [Z, P]),
+                     ("swin_seqattn_bwd", [Q] + [P] * 11 + [Z, P]),
+                     ("swin_kvcache_workspace_size", [C, ctypes.POINTER(Z)]),
+                     ("swin_kvcache_append", [C, ctypes.c_int32] + [P] * 8 + [Z, P]),
+                     ("swin_kvcache_decode", [C] + [P] * 12 + [Z, P]),
+                     ("swin_kvcache_evict", [C] + [P] * 10 + [Z, P])):
+            getattr(L, f).argtypes = a
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -324,3 +354,294 @@ def backward(desc, q, k, v, bias_table, dout, workspace=None):
     dT = torch.empty_like(bias_table)
     swin_wattn_bwd(desc, q, k, v, bias_table, dout, dq, dk, dv, dT, workspace)
     return dq, dk, dv, dT
+
+
+# ---- attention along a token sequence and its paged cache (include/swin_seqattn.h) ----
+# These calls run on the device their tensors are on (all on one), whatever the
+# current device is, and on `stream` or that device's current stream.
+def _dtype_code(dtype):
+    if dtype in ("bf16", torch.bfloat16, SWIN_DTYPE_BF16):
+        return SWIN_DTYPE_BF16
+    if dtype in ("f32", torch.float32, SWIN_DTYPE_F32):
+        return SWIN_DTYPE_F32
+    raise ValueError("dtype must be bf16 or f32, got %r" % (dtype,))
+
+
+def make_seq_desc(B, S, heads, head_dim, window, dtype, kv_heads=None, sinks=0, flags=0,
+                  q_stride=0, kv_stride=0):
+    """window 0: every earlier token is visible; kv_heads None: one per query
+    head; strides in elements between tokens, 0: contiguous."""
+    return SwinSeqattnDesc(B, S, heads, heads if kv_heads is None else kv_heads, head_dim, window,
+                           sinks, _dtype_code(dtype), flags, q_stride, kv_stride)
+
+
+def _token_stride(t):
+    """Elements from token to token of [B, S, heads, hd], 0 if contiguous."""
+    n = t.shape[2] * t.shape[3]
+    s = t.stride(1) if t.shape[1] > 1 else (t.stride(0) if t.shape[0] > 1 else n)
+    return 0 if s == n else s
+
+
+def seq_desc_for(q, k, window, sinks=0, flags=0):
+    """Description of tensors q [B, S, heads, hd] and k (or v)
+    [B, S, kv_heads, hd], parts of a wider projection included."""
+    return make_seq_desc(q.shape[0], q.shape[1], q.shape[2], q.shape[3], window, q.dtype,
+                         k.shape[2], sinks, flags, _token_stride(q), _token_stride(k))
+
+
+class _Call:
+    """Pointers of one call's tensors, all on one device."""
+
+    def __init__(self, elem):
+        self.elem, self.device = elem, None
+
+    def _on(self, t, dtype, name):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % name)
+        if t.dtype != dtype:
+            raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        if self.device is None:
+            self.device = t.device
+        elif t.device != self.device:
+            raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, self.device))
+
+    def dense(self, t, shape, name, dtype=None, optional=False):
+        if t is None:
+            if not optional:
+                raise ValueError("%s is missing" % name)
+            return None
+        self._on(t, dtype or self.elem, name)
+        if tuple(t.shape) != shape:
+            raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        return t.data_ptr()
+
+    def tokens(self, t, shape, stride, name, optional=False):
+        """[B, T, heads, hd] (or [B, heads, hd]) with tokens `stride` elements apart."""
+        if t is None:
+            if not optional:
+                raise ValueError("%s is missing" % name)
+            return None
+        self._on(t, self.elem, name)
+        if tuple(t.shape) != shape:
+            raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+        want = [shape[-1], 1]
+        stride = stride or shape[-2] * shape[-1]
+        want = ([shape[1] * stride, stride] if len(shape) == 4 else [stride]) + want
+        for n, have, need in zip(shape, t.stride(), want):
+            if n > 1 and have != need:
+                raise ValueError("%s has strides %s, the description says %s"
+                                 % (name, t.stride(), tuple(want)))
+        return t.data_ptr()
+
+    def run(self, name, workspace, stream, *args):
+        ws = self.dense(workspace, tuple(workspace.shape), "workspace", torch.uint8)
+        dev = self.device
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        elif stream.device != dev:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
+        fn = getattr(lib(), name)
+        if torch.cuda.current_device() == dev.index:
+            rc = fn(*args, ws, workspace.numel(), stream.cuda_stream)
+        else:
+            with torch.cuda.device(dev):
+                rc = fn(*args, ws, workspace.numel(), stream.cuda_stream)
+        if rc != SWIN_OK:
+            raise SwinWattnError(rc, name)
+
+
+def swin_seqattn_path(desc):
+    rc = lib().swin_seqattn_path(ctypes.byref(desc))
+    if rc < 0:
+        raise SwinWattnError(rc, "swin_seqattn_path")
+    return rc
+
+
+def _workspace_size(name, desc):
+    n = ctypes.c_size_t(0)
+    _check(getattr(lib(), name)(ctypes.byref(desc), ctypes.byref(n)), name)
+    return n.value
+
+
+def swin_seqattn_workspace_size(desc):
+    return _workspace_size("swin_seqattn_workspace_size", desc)
+
+
+def swin_kvcache_workspace_size(desc):
+    return _workspace_size("swin_kvcache_workspace_size", desc)
+
+
+def _new_ws(size, device):
+    """Only the header (the device status word) has to start as zeros."""
+    ws = torch.empty(size, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def new_seq_workspace(desc, device="cuda"):
+    """Caller-owned workspace of the size the library asks for."""
+    return _new_ws(swin_seqattn_workspace_size(desc), device)
+
+
+def new_cache_workspace(desc, device="cuda"):
+    """Caller-owned workspace of the size the library asks for."""
+    return _new_ws(swin_kvcache_workspace_size(desc), device)
+
+
+def _seq_shapes(d):
+    return ((d.B, d.S, d.heads, d.head_dim), (d.B, d.S, d.kv_heads, d.head_dim),
+            (d.B, d.S, d.heads))
+
+
+def swin_seqattn_fwd(desc, q, k, v, lengths, out, lse=None, workspace=None, stream=None):
+    c = _Call(_elem(desc))
+    sq, sk, sl = _seq_shapes(desc)
+    args = (c.tokens(q, sq, desc.q_stride, "q"), c.tokens(k, sk, desc.kv_stride, "k"),
+            c.tokens(v, sk, desc.kv_stride, "v"),
+            c.dense(lengths, (desc.B,), "lengths", torch.int32, optional=True),
+            c.dense(out, sq, "out"), c.dense(lse, sl, "lse", torch.float32, optional=True))
+    if workspace is None:
+        workspace = new_seq_workspace(desc, c.device)
+    c.run("swin_seqattn_fwd", workspace, stream, ctypes.byref(desc), *args)
+    return out
+
+
+def swin_seqattn_bwd(desc, q, k, v, lengths, out, lse, dout, dq, dk, dv, workspace=None,
+                     stream=None):
+    c = _Call(_elem(desc))
+    sq, sk, sl = _seq_shapes(desc)
+    args = (c.tokens(q, sq, desc.q_stride, "q"), c.tokens(k, sk, desc.kv_stride, "k"),
+            c.tokens(v, sk, desc.kv_stride, "v"),
+            c.dense(lengths, (desc.B,), "lengths", torch.int32, optional=True),
+            c.dense(out, sq, "out"), c.dense(lse, sl, "lse", torch.float32),
+            c.dense(dout, sq, "dout"), c.tokens(dq, sq, desc.q_stride, "dq"),
+            c.tokens(dk, sk, desc.kv_stride, "dk"), c.tokens(dv, sk, desc.kv_stride, "dv"))
+    if workspace is None:
+        workspace = new_seq_workspace(desc, c.device)
+    c.run("swin_seqattn_bwd", workspace, stream, ctypes.byref(desc), *args)
+    return dq, dk, dv
+
+
+def seq_forward(desc, q, k, v, lengths=None, want_lse=False, workspace=None):
+    sq, _, sl = _seq_shapes(desc)
+    out = torch.empty(sq, dtype=q.dtype, device=q.device)
+    lse = torch.empty(sl, dtype=torch.float32, device=q.device) if want_lse else None
+    swin_seqattn_fwd(desc, q, k, v, lengths, out, lse, workspace)
+    return (out, lse) if want_lse else out
+
+
+def seq_backward(desc, q, k, v, out, lse, dout, lengths=None, workspace=None):
+    """dq, dk, dv, laid out as the description lays out q, k and v: parts of one
+    [B, S, heads + 2 kv_heads, hd] buffer when its strides are that buffer's."""
+    B, S, H, K, hd = desc.B, desc.S, desc.heads, desc.kv_heads, desc.head_dim
+    new = lambda n: torch.empty((B, S, n, hd), dtype=q.dtype, device=q.device)
+    if desc.q_stride and desc.q_stride == desc.kv_stride == (H + 2 * K) * hd:
+        both = new(H + 2 * K)
+        dq, dk, dv = both[:, :, :H], both[:, :, H:H + K], both[:, :, H + K:]
+    else:
+        wide = lambda n, s: (new(n) if not s else torch.empty(
+            (B, S, s), dtype=q.dtype, device=q.device)[:, :, :n * hd].unflatten(2, (n, hd)))
+        dq, dk, dv = wide(H, desc.q_stride), wide(K, desc.kv_stride), wide(K, desc.kv_stride)
+    return swin_seqattn_bwd(desc, q, k, v, lengths, out, lse, dout, dq, dk, dv, workspace)
+
+
+def make_cache_desc(B, heads, head_dim, page_size, num_pages, max_pages, dtype, kv_heads=None,
+                    window=0, sinks=0, recent=0, budget=0, weights=False, q_stride=0,
+                    kv_stride=0):
+    """weights: cache_decode will accumulate attention weights."""
+    return SwinKvcacheDesc(B, heads, heads if kv_heads is None else kv_heads, head_dim, page_size,
+                           num_pages, max_pages, window, sinks, recent, budget,
+                           _dtype_code(dtype), SWIN_FLAG_KV_WEIGHTS if weights else 0, q_stride,
+                           kv_stride)
+
+
+def _cache_args(c, d, lengths, page_table, k_cache, v_cache):
+    cache = (d.num_pages, d.kv_heads, d.page_size, d.head_dim)
+    return (c.dense(lengths, (d.B,), "lengths", torch.int32),
+            c.dense(page_table, (d.B, d.max_pages), "page_table", torch.int32),
+            c.dense(k_cache, cache, "k_cache"), c.dense(v_cache, cache, "v_cache"))
+
+
+def _cache_weights(c, d, t, name, optional=True):
+    return c.dense(t, (d.B, d.kv_heads, d.max_pages * d.page_size), name, torch.float32, optional)
+
+
+def swin_kvcache_append(desc, k, v, counts, lengths, page_table, k_cache, v_cache,
+                        workspace=None, stream=None):
+    """k, v: [B, T, kv_heads, head_dim]."""
+    d, c = desc, _Call(_elem(desc))
+    T = k.shape[1] if k.dim() == 4 else 0
+    shape = (d.B, T, d.kv_heads, d.head_dim)
+    args = (T, c.tokens(k, shape, d.kv_stride, "k"), c.tokens(v, shape, d.kv_stride, "v"),
+            c.dense(counts, (d.B,), "counts", torch.int32, optional=True),
+            *_cache_args(c, d, lengths, page_table, k_cache, v_cache))
+    if workspace is None:
+        workspace = _new_ws(256, c.device)
+    c.run("swin_kvcache_append", workspace, stream, ctypes.byref(d), *args)
+
+
+def swin_kvcache_decode(desc, q, k_new, v_new, lengths, page_table, k_cache, v_cache, weights,
+                        new_weights, out, lse=None, workspace=None, stream=None):
+    d, c = desc, _Call(_elem(desc))
+    sk = (d.B, d.kv_heads, d.head_dim)
+    args = (c.tokens(q, (d.B, d.heads, d.head_dim), d.q_stride, "q"),
+            c.tokens(k_new, sk, d.kv_stride, "k_new", optional=True),
+            c.tokens(v_new, sk, d.kv_stride, "v_new", optional=True),
+            *_cache_args(c, d, lengths, page_table, k_cache, v_cache),
+            _cache_weights(c, d, weights, "weights"),
+            _cache_weights(c, d, new_weights, "new_weights"),
+            c.dense(out, (d.B, d.heads, d.head_dim), "out"),
+            c.dense(lse, (d.B, d.heads), "lse", torch.float32, optional=True))
+    if workspace is None:
+        workspace = new_cache_workspace(d, c.device)
+    c.run("swin_kvcache_decode", workspace, stream, ctypes.byref(d), *args)
+    return out
+
+
+def swin_kvcache_evict(desc, weights, lengths, page_table, dst_page_table, k_cache, v_cache,
+                       new_weights, new_lengths, kept=None, workspace=None, stream=None):
+    d, c = desc, _Call(_elem(desc))
+    n, t, kc, vc = _cache_args(c, d, lengths, page_table, k_cache, v_cache)
+    args = (_cache_weights(c, d, weights, "weights", False), n, t,
+            c.dense(dst_page_table, (d.B, d.max_pages), "dst_page_table", torch.int32), kc, vc,
+            _cache_weights(c, d, new_weights, "new_weights", False),
+            c.dense(new_lengths, (d.B,), "new_lengths", torch.int32),
+            c.dense(kept, (d.B, d.kv_heads, d.budget), "kept", torch.int32, optional=True))
+    if workspace is None:
+        workspace = new_cache_workspace(d, c.device)
+    c.run("swin_kvcache_evict", workspace, stream, ctypes.byref(d), *args)
+    return new_weights, new_lengths
+
+
+def cache_append(desc, k, v, lengths, page_table, k_cache, v_cache, counts=None, workspace=None):
+    """Writes tokens k, v [B, T, kv_heads, hd] to the cache's last positions;
+    `lengths` already counts them."""
+    swin_kvcache_append(desc, k, v, counts, lengths, page_table, k_cache, v_cache, workspace)
+
+
+def cache_decode(desc, q, lengths, page_table, k_cache, v_cache, k_new=None, v_new=None,
+                 weights=None, new_weights=None, want_lse=False, workspace=None):
+    """Attention of one token per sequence, q [B, heads, hd], over the cache.
+    With `weights` and no new_weights the step's weights are added in place."""
+    out = torch.empty((desc.B, desc.heads, desc.head_dim), dtype=q.dtype, device=q.device)
+    lse = (torch.empty((desc.B, desc.heads), dtype=torch.float32, device=q.device)
+           if want_lse else None)
+    if weights is not None and new_weights is None:
+        new_weights = weights
+    swin_kvcache_decode(desc, q, k_new, v_new, lengths, page_table, k_cache, v_cache, weights,
+                        new_weights, out, lse, workspace)
+    return (out, lse) if want_lse else out
+
+
+def cache_evict(desc, weights, lengths, page_table, dst_page_table, k_cache, v_cache,
+                new_weights=None, new_lengths=None, kept=None, workspace=None):
+    """Copies the positions that stay to dst_page_table's pages; returns
+    (new_weights, new_lengths)."""
+    if new_weights is None:
+        new_weights = torch.empty_like(weights)
+    if new_lengths is None:
+        new_lengths = torch.empty_like(lengths)
+    return swin_kvcache_evict(desc, weights, lengths, page_table, dst_page_table, k_cache, v_cache,
+                              new_weights, new_lengths, kept, workspace)

@@ -25,7 +25,8 @@ def _stale(lib):
         return True
     t = os.path.getmtime(lib)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(ROOT, "include", "swin_wattn.h"))
+    inc = os.path.join(ROOT, "include")
+    deps += [os.path.join(inc, f) for f in os.listdir(inc)]
     deps.append(__file__)
     return any(os.path.getmtime(d) > t for d in deps)
 
