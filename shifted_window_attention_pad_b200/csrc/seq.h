@@ -38,7 +38,8 @@ struct SeqParams {
   const float* lse_in;
   void *out, *dq, *dk, *dv;
   float* lse;
-  float2* ld;                      // backward: (lse * log2 e, D) [B][H][S]
+  float2* ld;                      // backward: (lse * log2 e, D) [B][H][ld_stride]
+  long long ld_stride;             // S rounded up to whole steps of 64 queries
   float *main_part, *sink_part;    // backward partials (see DkvPlan)
   DkvPlan plan;
   int* status;

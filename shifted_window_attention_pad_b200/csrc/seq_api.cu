@@ -67,6 +67,7 @@ SeqParams seq_params(const swin_seqattn_desc* d) {
   p.scale = 1.f / sqrtf((float)d->head_dim);
   p.scale_log2 = kSeqLog2e / sqrtf((float)d->head_dim);
   p.test_timeout = (d->flags & SWIN_FLAG_TEST_TIMEOUT) ? 1 : 0;
+  p.ld_stride = ((long long)d->S + 63) / 64 * 64;
   p.plan = make_dkv_plan(p.B, p.S, p.K, p.G, p.hd, p.window, p.sinks,
                          seq_fast(d) ? 128 : seq_generic_tile(p.hd));
   return p;
@@ -74,14 +75,14 @@ SeqParams seq_params(const swin_seqattn_desc* d) {
 
 // Header, (lse, D) of every row, partials of the key-side backward.
 size_t seq_workspace(const SeqParams& p) {
-  return kWsHeader + align256((size_t)p.B * p.H * p.S * 8) + align256(p.plan.main_bytes) +
+  return kWsHeader + align256((size_t)p.B * p.H * p.ld_stride * 8) + align256(p.plan.main_bytes) +
          align256(p.plan.sink_bytes);
 }
 void seq_carve(SeqParams& p, void* ws) {
   char* w = (char*)ws;
   p.status = (int*)w;
   p.ld = (float2*)(w += kWsHeader);
-  p.main_part = (float*)(w += align256((size_t)p.B * p.H * p.S * 8));
+  p.main_part = (float*)(w += align256((size_t)p.B * p.H * p.ld_stride * 8));
   p.sink_part = (float*)(w + align256(p.plan.main_bytes));
 }
 

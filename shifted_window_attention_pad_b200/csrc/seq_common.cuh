@@ -170,7 +170,7 @@ __device__ __noinline__ void fix_dq_row(const SeqParams& p, int b, int h, int i)
   fix_load(g, (const E*)p.dout + (((long long)b * p.S + i) * p.H + h) * p.hd, p.hd);
 #pragma unroll
   for (int t = 0; t < kFixT; ++t) acc[t] = 0.f;
-  const float2 ld = p.ld[((long long)b * p.H + h) * p.S + i];
+  const float2 ld = p.ld[((long long)b * p.H + h) * p.ld_stride + i];
   const int lo = max(0, i - p.window + 1);
   for (int j = p.sinks > 0 ? 0 : lo; j <= i; ++j) {
     if (j >= p.sinks && j < lo) j = lo;
@@ -199,7 +199,7 @@ __device__ __noinline__ void fix_dkv_row(const SeqParams& p, const DkvItem& it, 
       if (!seq_visible(p, it.n, i, j)) break;
       fix_load(x, (const E*)p.q + ((long long)it.b * p.S + i) * p.qs + (long long)h * p.hd, p.hd);
       fix_load(y, (const E*)p.dout + (((long long)it.b * p.S + i) * p.H + h) * p.hd, p.hd);
-      const float2 ld = p.ld[((long long)it.b * p.H + h) * p.S + i];
+      const float2 ld = p.ld[((long long)it.b * p.H + h) * p.ld_stride + i];
       const float w = exp2f(fix_dot(x, k) * p.scale_log2 - ld.x);
       const float ds = w * (fix_dot(y, v) - ld.y);
 #pragma unroll

@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThr) gen_dq_kernel(const __grid_constant__ Se
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[r][c] = 0.f;
     const int i = i0 + ty + 16 * r;
-    ld[r] = i < n ? p.ld[bh * p.S + i] : make_float2(0.f, 0.f);
+    ld[r] = i < n ? p.ld[bh * p.ld_stride + i] : make_float2(0.f, 0.f);
   }
   if (threadIdx.x < T) flags[threadIdx.x] = 0;
   if (i0 < n) {
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThr) gen_dkv_kernel(const __grid_constant__ S
                             (long long)p.H * p.hd, rows, p.hd);
         if (threadIdx.x < T)
           lds[threadIdx.x] = (int)threadIdx.x < rows
-                                 ? p.ld[((long long)it.b * p.H + h) * p.S + i0 + threadIdx.x]
+                                 ? p.ld[((long long)it.b * p.H + h) * p.ld_stride + i0 + threadIdx.x]
                                  : make_float2(0.f, 0.f);
         __syncthreads();
         float s[R][R], dp[R][R];
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ SeqPa
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
   if (lane == 0)
-    p.ld[((long long)b * p.H + h) * p.S + i] =
+    p.ld[((long long)b * p.H + h) * p.ld_stride + i] =
         real ? make_float2(p.lse_in[row] * kSeqLog2e, d) : make_float2(INFINITY, 0.f);
 }
 

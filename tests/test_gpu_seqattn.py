@@ -207,6 +207,18 @@ def test_two_streams_with_a_workspace_each():
             assert torch.equal(x, one[name]), name
 
 
+def test_timeouts_are_reported():
+    """The kernels' bounded wait: a barrier that nothing arrives on ends the call
+    with a status, and the workspace serves the next call."""
+    q, k, v, g = make(1, 200, 2, 2, 64, "bf16", seed=25)
+    d = sb.seq_desc_for(q, k, window=0, flags=sb.SWIN_FLAG_TEST_TIMEOUT)
+    ws = sb.new_seq_workspace(d)
+    sb.seq_forward(d, q, k, v, workspace=ws)
+    assert sb.swin_wattn_poll_status(ws) == sb.SWIN_ERR_TIMEOUT
+    assert sb.swin_wattn_poll_status(ws) == 0
+    ref.check(run(q, k, v, g, 0, 0, ws=ws), ref.attention(q, k, v, 0, 0, None, g), ALL)
+
+
 def test_wrappers_refuse_what_the_description_does_not_say():
     q, k, v, g = make(1, 40, 4, 2, 64, "bf16")
     d = sb.seq_desc_for(q, k, window=0)

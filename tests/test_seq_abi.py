@@ -101,6 +101,15 @@ def test_bad_dtype(L):
     assert sb.make_seq_desc(1, 1, 1, 64, 0, "f32").dtype == sb.SWIN_DTYPE_F32
 
 
+def test_paths(L):
+    for hd, dtype, want in ((64, "bf16", 1), (128, "bf16", 1), (80, "bf16", 0), (256, "bf16", 0),
+                            (64, "f32", 0)):
+        d = sb.make_seq_desc(1, 300, 4, hd, 0, dtype)
+        assert sb.swin_seqattn_path(d) == want, (hd, dtype)
+        d.flags = sb.SWIN_FLAG_FORCE_GENERIC
+        assert sb.swin_seqattn_path(d) == 0
+
+
 @pytest.mark.parametrize("bad", range(4))
 def test_forward_pointers(L, bad):
     d = ctypes.byref(_seq())
@@ -138,6 +147,23 @@ def test_backward_refuses_shared_outputs(L):
         a = [AT(z) for z in range(9)]
         a[x] = a[y]
         assert L.swin_seqattn_bwd(d, *a[:3], None, *a[3:], GOOD, BIG, None) == -1, (x, y)
+
+
+def test_workspace_grows_with_what_it_holds():
+    """Header and (lse, D) of every row; with few key heads, or sinks in front
+    of a long sequence, fp32 partials of dk and dv."""
+    a256 = lambda x: (x + 255) // 256 * 256
+    d = sb.make_seq_desc(8, 4096, 32, 64, 512, "bf16")
+    assert sb.swin_seqattn_workspace_size(d) == 256 + 8 * 4096 * 32 * 8
+    one = sb.make_seq_desc(1, 256, 4, 64, 0, "bf16", kv_heads=1)
+    assert sb.swin_seqattn_workspace_size(one) == 256 + a256(256 * 4 * 8) + 4 * 2 * 256 * 64 * 4
+    sinks = sb.make_seq_desc(8, 4096, 32, 64, 512, "bf16", sinks=4)
+    # one sink tile of 128 keys for each of 8 x 32 heads, four chunks of 1024 queries
+    assert (sb.swin_seqattn_workspace_size(sinks) - sb.swin_seqattn_workspace_size(d)
+            == 2 * 8 * 32 * 4 * 128 * 64 * 4)
+    # sinks that the window covers are no sinks
+    wide = sb.make_seq_desc(8, 4096, 32, 64, 4096, "bf16", sinks=4)
+    assert sb.swin_seqattn_workspace_size(wide) == sb.swin_seqattn_workspace_size(d)
 
 
 def test_cache_calls_refuse_bad_arguments(L):
