@@ -38,7 +38,7 @@ struct SeqParams {
   const float* lse_in;
   void *out, *dq, *dk, *dv;
   float* lse;
-  float2* ld;                      // backward: (lse * log2 e, D) [B][H][ld_stride]
+  float *nl, *nd;                  // backward: -lse log2 e and -D of every row, [B][H][ld_stride]
   long long ld_stride;             // S rounded up to whole steps of 64 queries
   float *main_part, *sink_part;    // backward partials (see DkvPlan)
   DkvPlan plan;
@@ -53,7 +53,7 @@ DkvPlan make_dkv_plan(int B, int S, int K, int G, int hd, int window, int sinks,
 int seq_generic_tile(int hd);
 cudaError_t seq_generic_forward(const SeqParams& p, int dtype, cudaStream_t st);
 cudaError_t seq_generic_backward(const SeqParams& p, int dtype, cudaStream_t st);
-// (lse, D) of every row into p.ld, and the sum of the partials: both families.
+// (-lse log2 e, -D) of every row, and the sum of the partials: both families.
 cudaError_t seq_prep(const SeqParams& p, int dtype, cudaStream_t st);
 cudaError_t seq_reduce(const SeqParams& p, int dtype, cudaStream_t st);
 

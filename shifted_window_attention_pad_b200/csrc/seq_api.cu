@@ -81,7 +81,8 @@ size_t seq_workspace(const SeqParams& p) {
 void seq_carve(SeqParams& p, void* ws) {
   char* w = (char*)ws;
   p.status = (int*)w;
-  p.ld = (float2*)(w += kWsHeader);
+  p.nl = (float*)(w += kWsHeader);
+  p.nd = p.nl + (size_t)p.B * p.H * p.ld_stride;
   p.main_part = (float*)(w += align256((size_t)p.B * p.H * p.ld_stride * 8));
   p.sink_part = (float*)(w + align256(p.plan.main_bytes));
 }

@@ -16,7 +16,7 @@
 //
 // D_i = dO_i.o_i uses the stored, rounded o. Where a row sees few keys its dS is
 // a small difference of dP and D and that rounding would show, so items of at
-// most kTwoPass key steps take D = sum_j P_ij dP_ij from a pass of their own
+// at most kFewKeys keys take D = sum_j P_ij dP_ij from a pass of their own
 // first (and leave it for the key side): an error of 0.11 of the gradients' RMS
 // in the first rows of a sequence becomes that of other rows. Longer rows would
 // pay two more products per step for an error already below the outputs' own
@@ -27,8 +27,7 @@
 // issues the gradient products. Bound: the tensor pipe (per 128 x 64 step of
 // head_dim 128: S and dP 384 cycles each, limited by shared-memory reads of
 // both operands, 256 for each gradient product).
-#include "fast_common.cuh"
-#include "seq_common.cuh"
+#include "seq_tc.cuh"
 
 namespace swin {
 namespace {
@@ -39,8 +38,17 @@ constexpr int kStep = 64;         // keys (queries) of a step
 constexpr int kSoft = 16;         // softmax warps
 constexpr int kBProducer = 16, kBMma = 17, kBMma2 = 18;
 constexpr int kBThreads = 19 * 32;
-constexpr int kTwoPass = 6;
-constexpr uint32_t kAccCol = 256;
+// TMEM: NB buffers of S | dP, then ND accumulators of HD columns (dQ) or 2 HD
+// (dV, dK). Three buffers let a step's products start while the two softmax
+// pairs work on those before; head_dim 128 leaves the key side two.
+template <int HD, bool KEYS>
+struct BwdTmem {
+  static constexpr int NB = KEYS && HD > 64 ? 2 : 3;
+  static constexpr int ND = KEYS || HD > 64 ? 1 : 2;
+  static constexpr uint32_t kAccCol = NB * 2 * kStep;
+  static constexpr uint32_t kAccCols = KEYS ? 2 * HD : HD;
+  static_assert(kAccCol + ND * kAccCols <= 512, "TMEM columns");
+};
 
 struct BwdMaps {
   CUtensorMap a0, a1, b0, b1;   // stationary pair, streamed pair
@@ -56,42 +64,10 @@ struct BwdCfg {
   static constexpr uint32_t kLd = kRing + kStages * 2 * kSub;
   static constexpr uint32_t kXch = kLd + kStages * kStep * 8;
   static constexpr uint32_t kBars = kXch + 4 * kRows * 4;
-  static constexpr uint32_t kTotal = kBars + 8 * 40 + 16;
+  static constexpr uint32_t kFeedAt = kBars + 8 * 40;
+  static constexpr uint32_t kTotal = kFeedAt + sizeof(Feed) + 16;
   static constexpr uint32_t kSmem = kTotal + 1024;
 };
-
-// Operands of 64-row tiles (channel halves of 64 as [64][64] regions).
-template <int HD>
-__device__ __forceinline__ uint64_t sub_kmajor(uint32_t base, int k16) {
-  return smem_desc(base + (k16 >> 2) * (kStep * 128) + (k16 & 3) * 32, 16, 1024, kSwizzle128);
-}
-template <int HD>
-__device__ __forceinline__ uint64_t sub_mnmajor(uint32_t base, int k16) {
-  return smem_desc(base + k16 * 16 * 128, HD > 64 ? kStep * 128 : 1024, 1024, kSwizzle128);
-}
-
-template <int ROWS, int HD>
-__device__ __forceinline__ void load_tokens(const CUtensorMap* m, uint8_t* dst, int h, int row,
-                                            int b, uint64_t* bar) {
-#pragma unroll
-  for (int hf = 0; hf < HD / 64; ++hf)
-    tma_load_4d(dst + hf * ROWS * 128, m, bar, hf * 64, h, row, b);
-}
-
-// Zeroes rows from .. 63 of a streamed tile (a warp; see seq_fwd_kernel).
-template <int HD>
-__device__ __forceinline__ void zero_sub_rows(uint8_t* tile, int from) {
-  const int lane = threadIdx.x & 31;
-  for (int hf = 0; hf < HD / 64; ++hf)
-    for (int x = from * 8 + lane; x < kStep * 8; x += 32)
-      st_shared_v4(smem_u32(tile + hf * kStep * 128 + x * 16), 0u, 0u, 0u, 0u);
-}
-
-__device__ __forceinline__ bool bwd_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                              int* status) {
-  const bool ok = mbar_wait(bar, parity, abort, status, kWaitLimitNs);
-  return __all_sync(0xffffffffu, ok);
-}
 
 // An item of either side, for every role alike: `steps` streamed tiles a pass.
 template <bool KEYS>
@@ -99,14 +75,38 @@ struct BwdItem {
   DkvItem d;             // key side
   KeyTiles kt;           // query side: key steps
   int b, h, r0, n;       // query side: head and first query; key side: r0 = first key
-  int steps, passes, per;   // per: steps of one query head (key side)
-  __device__ __forceinline__ int row(int x) const {   // first streamed token of step x
-    if constexpr (KEYS) return d.i0 + (x % per) * kStep;
-    else return kt.tile(x) * kStep;
+  int steps, passes;
+  // Whether the query rows of a step (key side: from `row`) see few keys (kFewKeys).
+  __device__ __forceinline__ bool few(const SeqParams& p, int row) const {
+    if constexpr (KEYS) return min(row + kStep, p.window + p.sinks) <= kFewKeys;
+    else return passes == 2;
   }
-  __device__ __forceinline__ int head(int x) const {   // query head of step x
-    if constexpr (KEYS) return d.h0 + x / per;
-    else return h;
+};
+// Walks an item's steps in order: first streamed token and query head of each.
+template <bool KEYS>
+struct StepWalk {
+  int row, head, x;
+  __device__ __forceinline__ void start(const BwdItem<KEYS>& it) {
+    x = 0;
+    if constexpr (KEYS) {
+      row = it.d.i0;
+      head = it.d.h0;
+    } else {
+      row = it.kt.tile(0) * kStep;
+      head = it.h;
+    }
+  }
+  __device__ __forceinline__ void next(const BwdItem<KEYS>& it) {
+    ++x;
+    row += kStep;
+    if constexpr (KEYS) {
+      if (row >= it.d.i1) {
+        row = it.d.i0;
+        ++head;
+      }
+    } else {
+      if (x == it.kt.s) row = it.kt.lo * kStep;
+    }
   }
 };
 template <bool KEYS>
@@ -114,17 +114,14 @@ __device__ __forceinline__ BwdItem<KEYS> bwd_item(const SeqParams& p, long long 
   BwdItem<KEYS> it;
   it.steps = 0;
   it.passes = 1;
-  it.per = 1;
   if constexpr (KEYS) {
     it.d = dkv_item(p, t);
     it.b = it.d.b;
     it.h = it.d.kh;
     it.n = it.d.n;
     it.r0 = it.d.tile * kRows;
-    if (it.d.i0 < it.d.i1) {
-      it.per = (it.d.i1 - it.d.i0 + kStep - 1) / kStep;
-      it.steps = it.per * (it.d.h1 - it.d.h0);
-    }
+    if (it.d.i0 < it.d.i1)
+      it.steps = (it.d.i1 - it.d.i0 + kStep - 1) / kStep * (it.d.h1 - it.d.h0);
   } else {
     const int bh = p.B * p.H, tiles = (p.S + kRows - 1) / kRows;
     const int r = (int)(t / bh), z = (int)(t - (long long)r * bh);
@@ -135,7 +132,7 @@ __device__ __forceinline__ BwdItem<KEYS> bwd_item(const SeqParams& p, long long 
     if (it.r0 < it.n) {
       it.kt = seq_key_tiles(p, it.r0, min(it.n, it.r0 + kRows), kStep);
       it.steps = it.kt.count();
-      it.passes = it.steps <= kTwoPass ? 2 : 1;
+      it.passes = it.steps * kStep <= kFewKeys ? 2 : 1;
     }
   }
   return it;
@@ -176,46 +173,50 @@ __device__ __forceinline__ bool store_grad(uint32_t col, float mul, bool keep, v
 
 template <int HD, bool KEYS>
 __global__ void __launch_bounds__(kBThreads, 1)
-    seq_bwd_kernel(const __grid_constant__ SeqParams p, const __grid_constant__ BwdMaps maps,
-                   const long long n_items) {
+    seq_bwd_kernel(const __grid_constant__ SeqParams p,
+                   const __grid_constant__ BwdMaps maps) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   using C = BwdCfg<HD>;
-  constexpr int NA = C::kABufs, NS = C::kStages;
+  using TM = BwdTmem<HD, KEYS>;
+  constexpr int NA = C::kABufs, NS = C::kStages, NB = TM::NB, ND = TM::ND;
   constexpr uint32_t TB = C::kTile, SB = C::kSub;
   uint8_t* abuf = smem;
   uint8_t* ring = smem + C::kRing;
-  float2* lds = (float2*)(smem + C::kLd);
+  float* lds = (float*)(smem + C::kLd);   // per stage: -L of 64 queries, -D
   float* xch = (float*)(smem + C::kXch);
   uint64_t* bars = (uint64_t*)(smem + C::kBars);
   uint64_t* a_full = bars;
   uint64_t* a_empty = a_full + NA;
   uint64_t* b_full = a_empty + NA;
   uint64_t* b_empty = b_full + NS;
-  uint64_t* s_full = b_empty + NS;    // [2] per TMEM buffer
-  uint64_t* p_full = s_full + 2;
-  uint64_t* g_done = p_full + 2;
-  uint64_t* acc_full = g_done + 2;
-  uint64_t* acc_empty = acc_full + 1;
-  uint64_t* drain = acc_empty + 1;    // [2]: one per MMA-issuing thread
+  uint64_t* s_full = b_empty + NS;    // [NB] per TMEM buffer
+  uint64_t* p_full = s_full + NB;
+  uint64_t* g_done = p_full + NB;
+  uint64_t* acc_full = g_done + NB;   // [ND] each
+  uint64_t* acc_empty = acc_full + ND;
+  uint64_t* drain = acc_empty + ND;   // [2]: one per MMA-issuing thread
   uint64_t* never = drain + 2;
-  uint32_t* tmem_slot = (uint32_t*)(smem + C::kBars + 8 * 40);
+  Feed* feed = (Feed*)(smem + C::kFeedAt);
+  uint32_t* tmem_slot = (uint32_t*)(smem + C::kFeedAt + sizeof(Feed));
   volatile int* abort = (volatile int*)(tmem_slot + 1);
-  static_assert(2 * NA + 2 * NS + 6 + 2 + 3 <= 40, "barriers");
+  static_assert(2 * NA + 2 * NS + 3 * NB + 2 * ND + 3 <= 40, "barriers");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NA; ++i) { mbar_init(&a_full[i], 1); mbar_init(&a_empty[i], 1); }
     // a stage is free once the gradient products and (key side) the readers of
     // its (L, D) are done: the latter arrive before p_full, which those wait for
     for (int i = 0; i < NS; ++i) { mbar_init(&b_full[i], 1); mbar_init(&b_empty[i], 1); }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 2 * kWg);
-      mbar_init(&g_done[i], 1); mbar_init(&drain[i], 1);
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 2 * kWg); mbar_init(&g_done[i], 1);
     }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 4 * kWg);
+    for (int i = 0; i < ND; ++i) {
+      mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4 * kWg);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
     mbar_init(never, 1);
+    feed_init(feed, 3 + kSoft);   // producer, two MMA warps, the softmax warps
     *abort = 0;
     fence_mbar_init();
   }
@@ -233,39 +234,52 @@ __global__ void __launch_bounds__(kBThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  FeedRead rd{{}, feed, 0};
+  long long t = blockIdx.x;
 
   if (warp == kBProducer) {
     if (lane == 0) {
+      Ring<NA> ra;
+      Ring<NS> rb;
       long long k = 0, e = 0;   // items with work, stages filled
+      FeedAsk ask{{}, feed, 0};
       bool ok = true;
-      for (long long t = blockIdx.x; t < n_items && ok; t += gridDim.x) {
+      do {
         const BwdItem<KEYS> it = bwd_item<KEYS>(p, t);
         if (!it.steps) continue;
-        const int as = (int)(k % NA);
-        if (!mbar_wait(&a_empty[as], (uint32_t)(((k / NA) & 1) ^ 1), abort, p.status,
-                       kWaitLimitNs))
-          break;
-        mbar_arrive_expect_tx(&a_full[as], 2 * TB);
-        load_tokens<kRows, HD>(&maps.a0, abuf + as * 2 * TB, it.h, it.r0, it.b, &a_full[as]);
-        load_tokens<kRows, HD>(&maps.a1, abuf + as * 2 * TB + TB, it.h, it.r0, it.b, &a_full[as]);
+        uint8_t* a = abuf + ra.s * 2 * TB;
+        uint64_t* af = &a_full[ra.s];
+        if (!seq_wait(&a_empty[ra.s], ra.parity ^ 1, abort, p.status)) break;
+        mbar_arrive_expect_tx(af, 2 * TB);
+        load_tokens<kRows, HD>(&maps.a0, a, it.h, it.r0, it.b, af);
+        load_tokens<kRows, HD>(&maps.a1, a + TB, it.h, it.r0, it.b, af);
+        ra.next();
         ++k;
-        for (int x = 0; x < it.steps * it.passes; ++x, ++e) {
-          const int s = (int)(e % NS), u = x % it.steps, row = it.row(u);
-          const int h = KEYS ? it.head(u) : it.h / p.G;
-          if (!mbar_wait(&b_empty[s], (uint32_t)(((e / NS) & 1) ^ 1), abort, p.status,
-                         kWaitLimitNs)) {
-            ok = false;
-            break;
+        const int kh = it.h / p.G;
+        for (int ps = 0; ps < it.passes && ok; ++ps) {
+          StepWalk<KEYS> w;
+          for (w.start(it); w.x < it.steps; w.next(it), rb.next(), ++e) {
+            if (!seq_wait(&b_empty[rb.s], rb.parity ^ 1, abort, p.status)) {
+              ok = false;
+              break;
+            }
+            uint64_t* bf = &b_full[rb.s];
+            uint8_t* d = ring + rb.s * 2 * SB;
+            const int h = KEYS ? w.head : kh;
+            mbar_arrive_expect_tx(bf, 2 * SB + (KEYS ? kStep * 8 : 0));
+            load_tokens<kStep, HD>(&maps.b0, d, h, w.row, it.b, bf);
+            load_tokens<kStep, HD>(&maps.b1, d + SB, h, w.row, it.b, bf);
+            if constexpr (KEYS) {   // rows of nl, nd are padded to whole steps
+              const long long at = ((long long)it.b * p.H + h) * p.ld_stride + w.row;
+              bulk_load(lds + rb.s * 2 * kStep, p.nl + at, kStep * 4, bf);
+              bulk_load(lds + rb.s * 2 * kStep + kStep, p.nd + at, kStep * 4, bf);
+            }
           }
-          mbar_arrive_expect_tx(&b_full[s], 2 * SB + (KEYS ? kStep * 8 : 0));
-          load_tokens<kStep, HD>(&maps.b0, ring + s * 2 * SB, h, row, it.b, &b_full[s]);
-          load_tokens<kStep, HD>(&maps.b1, ring + s * 2 * SB + SB, h, row, it.b, &b_full[s]);
-          if constexpr (KEYS)   // rows of p.ld are padded to whole steps
-            bulk_load(lds + s * kStep, p.ld + ((long long)it.b * p.H + h) * p.ld_stride + row,
-                      kStep * 8, &b_full[s]);
         }
-      }
+        // (asked when the item's loads are out: see seq_fwd_kernel)
+      } while (ok && ask.ask(abort, p.status) && rd.next<false>(&t, abort, p.status));
       if (*abort) {
+        feed_drain(ask, rd);
         for (long long j = (e > NS ? e - NS : 0); j < e; ++j)
           mbar_drain(&b_full[j % NS], (uint32_t)((j / NS) & 1), kTestLimitNs * 100);
         for (long long j = (k > NA ? k - NA : 0); j < k; ++j)
@@ -273,107 +287,114 @@ __global__ void __launch_bounds__(kBThreads, 1)
       }
     }
   } else if (warp == kBMma) {
-    if (lane == 0) {   // S = A0 B0^T and dP = A1 B1^T of each step
-      constexpr uint32_t idesc = idesc_bf16(kRows, kStep, 0, 0);
-      long long k = 0, e = 0;
-      uint32_t nb[2] = {0, 0};
-      bool ok = true;
-      for (long long t = blockIdx.x; t < n_items && ok; t += gridDim.x) {
-        const BwdItem<KEYS> it = bwd_item<KEYS>(p, t);
-        if (!it.steps) continue;
-        const int as = (int)(k % NA);
-        if (!mbar_wait(&a_full[as], (uint32_t)((k / NA) & 1), abort, p.status, kWaitLimitNs))
-          break;
-        const uint32_t a0 = smem_u32(abuf + as * 2 * TB), a1 = a0 + TB;
-        for (int x = 0; x < it.steps * it.passes; ++x, ++e) {
-          const int s = (int)(e % NS), b = (int)(e & 1);
-          // the buffer is free once its previous gradient products are done
-          if (!mbar_wait(&b_full[s], (uint32_t)((e / NS) & 1), abort, p.status, kWaitLimitNs) ||
-              !mbar_wait(&g_done[b], (nb[b] & 1) ^ 1, abort, p.status, kWaitLimitNs)) {
-            ok = false;
-            break;
-          }
-          ++nb[b];
-          tc_fence_after();
-          const uint32_t b0 = smem_u32(ring + s * 2 * SB), b1 = b0 + SB;
-          const uint32_t d = tmem + b * 128;
-#pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk)
-            umma_ss(d, desc_kmajor_tile<HD>(a0, kk), sub_kmajor<HD>(b0, kk), idesc, kk);
-#pragma unroll
-          for (int kk = 0; kk < HD / 16; ++kk)
-            umma_ss(d + 64, desc_kmajor_tile<HD>(a1, kk), sub_kmajor<HD>(b1, kk), idesc, kk);
-          umma_commit(&s_full[b]);
-        }
-        if (ok) umma_commit(&a_empty[as]);
-        ++k;
-      }
-      if (*abort) {
-        umma_commit(&drain[0]);
-        mbar_drain(&drain[0], 0, kTestLimitNs * 100);
-      }
-    }
-  } else if (warp == kBMma2) {
-    // dQ += dS K, or dV += P^T dO and dK += dS^T Q (all lanes walk along: they
-    // zero the padding rows of a last streamed pair)
-    constexpr uint32_t idesc = idesc_bf16(kRows, HD, 0, 1);
-    long long k = 0, e = 0;
-    uint32_t nb[2] = {0, 0};
+    // S = A0 B0^T and dP = A1 B1^T of each step (the whole warp walks along, one
+    // elected lane issues)
+    constexpr uint32_t idesc = idesc_bf16(kRows, kStep, 0, 0);
+    Ring<NA> ra;
+    Ring<NS> rb;
+    Ring<NB> buf;    // TMEM buffers in turn
+    const uint32_t as = smem_u32(abuf), bs = smem_u32(ring);
     bool ok = true;
-    for (long long t = blockIdx.x; t < n_items && ok; t += gridDim.x) {
+    do {
       const BwdItem<KEYS> it = bwd_item<KEYS>(p, t);
       if (!it.steps) continue;
-      bool first = true;
-      for (int x = 0; x < it.steps * it.passes; ++x, ++e) {
-        const int s = (int)(e % NS), b = (int)(e & 1);
-        const bool grads = x >= it.steps * (it.passes - 1);
-        if (!bwd_warp_wait(&b_full[s], (uint32_t)((e / NS) & 1), abort, p.status)) {
-          ok = false;
-          break;
-        }
-        const int row = it.row(x % it.steps);
-        if (grads && row + kStep > it.n) {
-          zero_sub_rows<HD>(ring + s * 2 * SB, it.n - row);
-          zero_sub_rows<HD>(ring + s * 2 * SB + SB, it.n - row);
-          fence_proxy_async();
-          __syncwarp();
-        }
-        if ((first && grads &&
-             !bwd_warp_wait(acc_empty, (uint32_t)((k & 1) ^ 1), abort, p.status)) ||
-            !bwd_warp_wait(&p_full[b], nb[b] & 1, abort, p.status)) {
-          ok = false;
-          break;
-        }
-        ++nb[b];
+      if (!warp_wait(&a_full[ra.s], ra.parity, abort, p.status)) break;
+      const uint32_t a_at = uniform(as + ra.s * 2 * TB);
+      const uint64_t a0 = kmajor_base(a_at), a1 = kmajor_base(a_at + TB);
+      for (int x = it.steps * it.passes; x > 0; --x, rb.next(), buf.next()) {
+        // the buffer is free once its previous gradient products are done
+        ok = warp_wait(&b_full[rb.s], rb.parity, abort, p.status) &&
+             warp_wait(&g_done[buf.s], buf.parity ^ 1, abort, p.status);
+        if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
-          if (grads) {
-            const uint32_t b0 = smem_u32(ring + s * 2 * SB), b1 = b0 + SB;
-            const uint32_t d = tmem + b * 128;
-            // A from TMEM: 16 elements of K are 8 columns; the two column halves
-            // of a step sit 32 columns apart
+        const uint32_t b_at = uniform(bs + rb.s * 2 * SB);
+        const uint64_t b0 = kmajor_base(b_at), b1 = kmajor_base(b_at + SB);
+        const uint32_t d = uniform(tmem + buf.s * 2 * kStep);
+        if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kStep / 16; ++kk) {
-              const uint32_t a = d + 32 * (kk >> 1) + 8 * (kk & 1);
-              const uint32_t acc = (!first || kk > 0) ? 1u : 0u;
-              if constexpr (KEYS) {
-                umma_ts(tmem + kAccCol, a, sub_mnmajor<HD>(b1, kk), idesc, acc);
-                umma_ts(tmem + kAccCol + HD, a + 64, sub_mnmajor<HD>(b0, kk), idesc, acc);
-              } else {
-                umma_ts(tmem + kAccCol, a, sub_mnmajor<HD>(b0, kk), idesc, acc);
-              }
-            }
-          }
-          umma_commit(&b_empty[s]);
-          umma_commit(&g_done[b]);
+          for (int kk = 0; kk < HD / 16; ++kk)
+            umma_ss(d, a0 + kmajor_step<kRows>(kk), b0 + kmajor_step<kStep>(kk), idesc, kk > 0);
+#pragma unroll
+          for (int kk = 0; kk < HD / 16; ++kk)
+            umma_ss(d + kStep, a1 + kmajor_step<kRows>(kk), b1 + kmajor_step<kStep>(kk), idesc,
+                    kk > 0);
+          umma_commit(&s_full[buf.s]);
         }
         __syncwarp();
-        if (grads) first = false;
       }
-      if (ok && lane == 0) umma_commit(acc_full);
+      if (ok && elect_one()) umma_commit(&a_empty[ra.s]);
       __syncwarp();
-      ++k;
+      ra.next();
+    } while (ok && rd.next<true>(&t, abort, p.status));
+    if (*abort && lane == 0) {
+      umma_commit(&drain[0]);
+      mbar_drain(&drain[0], 0, kTestLimitNs * 100);
     }
+  } else if (warp == kBMma2) {
+    // dQ += dS K, or dV += P^T dO and dK += dS^T Q (the lanes also zero the padding
+    // rows of a last streamed pair)
+    constexpr uint32_t idesc = idesc_bf16(kRows, HD, 0, 1);
+    Ring<NS> rb;
+    Ring<NB> buf;
+    Ring<ND> acc;
+    const uint32_t bs = smem_u32(ring);
+    bool ok = true;
+    do {
+      const BwdItem<KEYS> it = bwd_item<KEYS>(p, t);
+      if (!it.steps) continue;
+      uint32_t on = 0;   // products add to the accumulators
+      for (int ps = 0; ps < it.passes && ok; ++ps) {
+        const bool grads = ps == it.passes - 1;
+        if (grads) ok = warp_wait(&acc_empty[acc.s], acc.parity ^ 1, abort, p.status);
+        const uint32_t to = uniform(tmem + TM::kAccCol + acc.s * TM::kAccCols);
+        StepWalk<KEYS> w;
+        for (w.start(it); ok && w.x < it.steps; w.next(it), rb.next(), buf.next()) {
+          ok = warp_wait(&b_full[rb.s], rb.parity, abort, p.status);
+          if (!ok) break;
+          if (grads && w.row + kStep > it.n) {
+            zero_rows<kStep, HD>(ring + rb.s * 2 * SB, it.n - w.row);
+            zero_rows<kStep, HD>(ring + rb.s * 2 * SB + SB, it.n - w.row);
+            fence_proxy_async();
+            __syncwarp();
+          }
+          ok = warp_wait(&p_full[buf.s], buf.parity, abort, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t b_at = uniform(bs + rb.s * 2 * SB);
+          const uint64_t b0 = mnmajor_base<kStep, HD>(b_at), b1 = mnmajor_base<kStep, HD>(b_at + SB);
+          const uint32_t d = uniform(tmem + buf.s * 2 * kStep);
+          const bool few = it.few(p, w.row);
+          if (elect_one()) {
+            if (grads) {
+              // A from TMEM: 16 elements of K are 8 columns; the two column halves
+              // of a step sit 32 columns apart, their low parts 16 behind the high
+#pragma unroll
+              for (int part = 0; part < 2; ++part) {
+                if (part && !few) break;
+#pragma unroll
+                for (int kk = 0; kk < kStep / 16; ++kk) {
+                  const uint32_t a = d + 32 * (kk >> 1) + 8 * (kk & 1) + 16 * part;
+                  const uint32_t add = on | (part > 0) | (kk > 0);
+                  if constexpr (KEYS) {
+                    umma_ts(to, a, b1 + mnmajor_step(kk), idesc, add);
+                    umma_ts(to + HD, a + kStep, b0 + mnmajor_step(kk), idesc, add);
+                  } else {
+                    umma_ts(to, a, b0 + mnmajor_step(kk), idesc, add);
+                  }
+                }
+              }
+            }
+            umma_commit(&b_empty[rb.s]);
+            umma_commit(&g_done[buf.s]);
+          }
+          __syncwarp();
+          on |= grads;
+        }
+      }
+      if (ok && elect_one()) umma_commit(&acc_full[acc.s]);
+      __syncwarp();
+      acc.next();
+    } while (ok && rd.next<true>(&t, abort, p.status));
     if (*abort && lane == 0) {
       umma_commit(&drain[1]);
       mbar_drain(&drain[1], 0, kTestLimitNs * 100);
@@ -381,43 +402,55 @@ __global__ void __launch_bounds__(kBThreads, 1)
   } else if (warp < kSoft) {
     // Warpgroup wg: buffer wg >> 1, columns 32 (wg & 1) .. of its steps; thread =
     // row (query or key) = TMEM lane.
-    const int wg = warp >> 2, buf = wg >> 1, half = wg & 1;
+    const int wg = warp >> 2, pair = wg >> 1, half = wg & 1;
     const int row = threadIdx.x & (kWg - 1);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_col = tmem + lane_base + buf * 128 + 32 * half;
     const float c = p.scale_log2;
-    long long e = 0, k = 0;
-    uint32_t nb = 0;
-    for (long long t = blockIdx.x; t < n_items; t += gridDim.x) {
-      if (named_sync_or(1, kSoft * 32, *abort)) break;
+    Ring<NS> rb;
+    Ring<NB> rbuf;
+    Ring<ND> racc;
+    uint32_t turn = 0;   // steps so far: the pairs take them in turn
+    bool more = true;
+    for (;;) {
+      // (barriers are waited for by parity: a pair waits for S of every second step
+      // only, but products are issued in order, and S of step e + NB not before the
+      // pair of step e has written P, so no round can be mistaken for another)
+      // all softmax warps go on together
+      if (named_sync_or(1, kSoft * 32, !more || *abort)) break;
       const BwdItem<KEYS> it = bwd_item<KEYS>(p, t);
       const int r = it.r0 + row;
       const bool stored = r < p.S, real = r < it.n;
       if (p.test_timeout && it.steps) mbar_wait(never, 0, abort, p.status, kTestLimitNs);
-      float2 ld = make_float2(0.f, 0.f);
+      float nl = 0.f, nd = 0.f;
       const long long ld_at = ((long long)it.b * p.H + it.h) * p.ld_stride + r;
       if constexpr (!KEYS) {
-        if (real) ld = p.ld[ld_at];
+        if (real) {
+          nl = p.nl[ld_at];
+          nd = p.nd[ld_at];
+        }
       }
       float dsum = 0.f;
-      for (int x = 0; x < it.steps * it.passes; ++x, ++e) {
-        if (!KEYS && it.passes == 2 && x == it.steps) {
+      StepWalk<KEYS> w;
+      if (it.steps) w.start(it);
+      for (int x = 0; x < it.steps * it.passes; ++x, ++turn, w.next(it), rb.next(), rbuf.next()) {
+        if (!KEYS && x == it.steps) {
+          w.start(it);
           // D of the row: the four warpgroups' parts, in order
           xch[wg * kRows + row] = dsum;
           named_sync(1, kSoft * 32);
-          ld.y = (xch[row] + xch[kRows + row]) + (xch[2 * kRows + row] + xch[3 * kRows + row]);
-          if (wg == 0 && real) p.ld[ld_at] = ld;
+          nd = -((xch[row] + xch[kRows + row]) + (xch[2 * kRows + row] + xch[3 * kRows + row]));
+          if (wg == 0 && real) p.nd[ld_at] = nd;
         }
-        if ((int)(e & 1) != buf) continue;
-        const int s = (int)(e % NS);
-        const int c0 = it.row(x % it.steps) + 32 * half;   // first token of these columns
-        mbar_wait(&s_full[buf], nb & 1, abort, p.status, kWaitLimitNs);
-        ++nb;
+        if ((int)(turn & 1) != pair) continue;
+        const uint32_t s_col = tmem + lane_base + rbuf.s * 2 * kStep + 32 * half;
+        const int s = rb.s;
+        const int c0 = w.row + 32 * half;   // first token of these columns
+        seq_wait(&s_full[rbuf.s], rbuf.parity, abort, p.status);
         tc_fence_after();
         float v[32], g[32];
         __syncwarp();
         tmem_ld32(s_col, v);
-        tmem_ld32(s_col + 64, g);
+        tmem_ld32(s_col + kStep, g);
         tmem_wait_ld_regs(v);
         reg_fence32(g);
         // visible columns of the row: lo .. hi, and below sk
@@ -435,41 +468,45 @@ __global__ void __launch_bounds__(kBThreads, 1)
           sk = p.sinks - c0;
           plain = c0 + 31 <= it.r0 && (it.r0 + kRows - 1 - c0 < p.window || c0 + 32 <= p.sinks);
         }
-        if constexpr (KEYS) {
-          const float4* ldv = reinterpret_cast<const float4*>(lds + s * kStep + 32 * half);
+        const bool sums = !KEYS && it.passes == 2 && x < it.steps;   // the pass for D
+        const float2 c2 = make_float2(c, c);
+        const float4* lv = reinterpret_cast<const float4*>(lds + s * 2 * kStep + 32 * half);
+        const float4* dv = lv + kStep / 4;
+        const float sub = sums ? 0.f : nd;
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float4 q = ldv[j / 2];   // L, D of two queries
-            const float2 a = __ffma2_rn(make_float2(v[j], v[j + 1]), make_float2(c, c),
-                                        make_float2(-q.x, -q.z));
-            v[j] = ex2(a.x);
-            v[j + 1] = ex2(a.y);
-            g[j] = g[j] - q.y;
-            g[j + 1] = g[j + 1] - q.w;
+        for (int j = 0; j < 32; j += 4) {
+          float4 l4 = make_float4(nl, nl, nl, nl), d4 = make_float4(sub, sub, sub, sub);
+          if constexpr (KEYS) {   // of four queries
+            l4 = lv[j / 4];
+            d4 = dv[j / 4];
           }
-        } else {
-          const float2 nl = make_float2(-ld.x, -ld.x);
-          const float sub = it.passes == 2 && x < it.steps ? 0.f : ld.y;
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float2 a = __ffma2_rn(make_float2(v[j], v[j + 1]), make_float2(c, c), nl);
-            v[j] = ex2(a.x);
-            v[j + 1] = ex2(a.y);
-            g[j] = g[j] - sub;
-            g[j + 1] = g[j + 1] - sub;
-          }
+          const float2 a = __ffma2_rn(make_float2(v[j], v[j + 1]), c2, make_float2(l4.x, l4.y));
+          const float2 b = __ffma2_rn(make_float2(v[j + 2], v[j + 3]), c2, make_float2(l4.z, l4.w));
+          v[j] = ex2(a.x);
+          v[j + 1] = ex2(a.y);
+          v[j + 2] = ex2(b.x);
+          v[j + 3] = ex2(b.y);
+          const float2 ga = __fmul2_rn(
+              __fadd2_rn(make_float2(g[j], g[j + 1]), make_float2(d4.x, d4.y)),
+              make_float2(v[j], v[j + 1]));
+          const float2 gb = __fmul2_rn(
+              __fadd2_rn(make_float2(g[j + 2], g[j + 3]), make_float2(d4.z, d4.w)),
+              make_float2(v[j + 2], v[j + 3]));
+          g[j] = ga.x;
+          g[j + 1] = ga.y;
+          g[j + 2] = gb.x;
+          g[j + 3] = gb.y;
         }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) g[j] *= v[j];
         if (!plain) {
+          const uint32_t see = column_mask(lo, hi, sk);
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (KEYS ? (j < lo || j > hi) : (j > hi || (j < lo && j >= sk))) {
+            if (!(see & (1u << j))) {
               v[j] = 0.f;
               g[j] = 0.f;
             }
         }
-        if (!KEYS && it.passes == 2 && x < it.steps) {
+        if (sums) {
           float a0 = 0.f, a1 = 0.f;
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
@@ -478,39 +515,46 @@ __global__ void __launch_bounds__(kBThreads, 1)
           }
           dsum += a0 + a1;
         } else {
-          uint32_t w[16];
-          if constexpr (KEYS) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+          constexpr int kDs = KEYS ? kStep : 0;   // dS over dP (key side) or S
+          if (it.few(p, w.row)) {
+            if constexpr (KEYS) split_to_columns(s_col, v);
+            split_to_columns(s_col + kDs, g);
+          } else {
+            uint32_t pk[16];
+            if constexpr (KEYS) {
+              round_pairs(v, pk);
+              __syncwarp();
+              tmem_st16u(s_col, pk);
+            }
+            round_pairs(g, pk);
             __syncwarp();
-            tmem_st16u(s_col, w);
+            tmem_st16u(s_col + kDs, pk);
           }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) w[j] = pack_bf16(g[2 * j], g[2 * j + 1]);
-          __syncwarp();
-          tmem_st16u(KEYS ? s_col + 64 : s_col, w);
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(&p_full[buf]);
+        mbar_arrive(&p_full[rbuf.s]);
       }
       // epilogue: each warpgroup a quarter of the accumulator columns
       constexpr int NC = KEYS ? HD / 2 : HD / 4;
       if (it.steps) {
-        mbar_wait(acc_full, (uint32_t)(k & 1), abort, p.status, kWaitLimitNs);
+        seq_wait(&acc_full[racc.s], racc.parity, abort, p.status);
         tc_fence_after();
-        ++k;
       }
-      const uint32_t acc = tmem + lane_base + kAccCol + wg * NC;
+      // (the item again, rather than kept in registers through the steps)
+      if constexpr (KEYS) asm volatile("" : "+l"(t));
+      const BwdItem<KEYS> at = bwd_item<KEYS>(p, t);
+      const uint32_t acc = tmem + lane_base + TM::kAccCol + racc.s * TM::kAccCols + wg * NC;
       void* dst;
       bool f32 = false;
       float mul = p.scale;
       if constexpr (KEYS) {
         const int off = (wg & 1) * NC;   // dV, dV, dK, dK
-        const long long at = ((long long)it.b * p.S + r) * p.ks + (long long)it.h * HD + off;
-        f32 = it.d.partial;
-        if (f32) dst = (wg < 2 ? it.d.pv : it.d.pk) + row * it.d.row_stride + off;
-        else dst = (__nv_bfloat16*)(wg < 2 ? p.dv : p.dk) + at;
+        f32 = at.d.partial;
+        if (f32) dst = (wg < 2 ? at.d.pv : at.d.pk) + row * at.d.row_stride + off;
+        else
+          dst = (__nv_bfloat16*)(wg < 2 ? p.dv : p.dk) +
+                ((long long)at.b * p.S + r) * p.ks + (long long)at.h * HD + off;
         if (wg < 2) mul = 1.f;
       } else {
         dst = (__nv_bfloat16*)p.dq + ((long long)it.b * p.S + r) * p.qs + (long long)it.h * HD +
@@ -521,7 +565,8 @@ __global__ void __launch_bounds__(kBThreads, 1)
       const bool bad = store_grad<NC>(acc, mul, real && it.steps, dst, f32) && real && it.steps;
       if (it.steps) {
         tc_fence_before();
-        mbar_arrive(acc_empty);
+        mbar_arrive(&acc_empty[racc.s]);
+        racc.next();
       }
       if (named_sync_or(1, kSoft * 32, bad && !*abort)) {
         int* flags = (int*)xch;
@@ -531,11 +576,12 @@ __global__ void __launch_bounds__(kBThreads, 1)
         named_sync(1, kSoft * 32);
         for (int y = warp; y < kRows; y += kSoft)
           if (flags[y]) {
-            if constexpr (KEYS) fix_dkv_row<__nv_bfloat16>(p, it.d, it.r0 + y);
+            if constexpr (KEYS) fix_dkv_row<__nv_bfloat16>(p, at.d, at.r0 + y);
             else fix_dq_row<__nv_bfloat16>(p, it.b, it.h, it.r0 + y);
           }
         named_sync(1, kSoft * 32);
       }
+      more = rd.next<true>(&t, abort, p.status);
     }
   }
   tc_fence_before();
@@ -544,22 +590,6 @@ __global__ void __launch_bounds__(kBThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-}
-
-// The map [hd, heads, S, B] of one operand, box [64, 1, rows, 1].
-bool encode_rows(CUtensorMap* m, const void* base, const SeqParams& p, int heads,
-                 long long stride, int rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)p.hd, (cuuint64_t)heads, (cuuint64_t)p.S,
-                              (cuuint64_t)p.B};
-  const cuuint64_t strides[3] = {(cuuint64_t)p.hd * 2, (cuuint64_t)stride * 2,
-                                 (cuuint64_t)stride * 2 * p.S};
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int HD, bool KEYS>
@@ -571,8 +601,8 @@ cudaError_t bwd_launch(const SeqParams& p, const BwdMaps& maps, cudaStream_t st)
   if (e != cudaSuccess) return e;
   const long long items =
       KEYS ? p.plan.items : (long long)p.B * p.H * ((p.S + kRows - 1) / kRows);
-  const int sms = num_sms();
-  kernel<<<(unsigned)(items < sms ? items : sms), kBThreads, smem, st>>>(p, maps, items);
+  if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  kernel<<<(unsigned)items, kBThreads, smem, st>>>(p, maps);
   note_launch();
   return cudaGetLastError();
 }
@@ -582,14 +612,14 @@ cudaError_t bwd_launch(const SeqParams& p, const BwdMaps& maps, cudaStream_t st)
 cudaError_t seq_fast_backward(const SeqParams& p, cudaStream_t st) {
   BwdMaps q, k;
   const long long os = (long long)p.H * p.hd;
-  if (!encode_rows(&q.a0, p.q, p, p.H, p.qs, kRows) ||
-      !encode_rows(&q.a1, p.dout, p, p.H, os, kRows) ||
-      !encode_rows(&q.b0, p.k, p, p.K, p.ks, kStep) ||
-      !encode_rows(&q.b1, p.v, p, p.K, p.ks, kStep) ||
-      !encode_rows(&k.a0, p.k, p, p.K, p.ks, kRows) ||
-      !encode_rows(&k.a1, p.v, p, p.K, p.ks, kRows) ||
-      !encode_rows(&k.b0, p.q, p, p.H, p.qs, kStep) ||
-      !encode_rows(&k.b1, p.dout, p, p.H, os, kStep))
+  if (!encode_tokens(&q.a0, p.q, p, p.H, p.qs, kRows) ||
+      !encode_tokens(&q.a1, p.dout, p, p.H, os, kRows) ||
+      !encode_tokens(&q.b0, p.k, p, p.K, p.ks, kStep) ||
+      !encode_tokens(&q.b1, p.v, p, p.K, p.ks, kStep) ||
+      !encode_tokens(&k.a0, p.k, p, p.K, p.ks, kRows) ||
+      !encode_tokens(&k.a1, p.v, p, p.K, p.ks, kRows) ||
+      !encode_tokens(&k.b0, p.q, p, p.H, p.qs, kStep) ||
+      !encode_tokens(&k.b1, p.dout, p, p.H, os, kStep))
     return cudaErrorInvalidValue;
   const cudaError_t e =
       p.hd == 64 ? bwd_launch<64, false>(p, q, st) : bwd_launch<128, false>(p, q, st);

@@ -99,6 +99,14 @@ __device__ __forceinline__ DkvItem dkv_item(const SeqParams& p, long long id) {
   return it;
 }
 
+// Bits lo .. hi of 32 columns and those below sk.
+__device__ __forceinline__ uint32_t below(int n) {   // bits 0 .. n - 1
+  return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+__device__ __forceinline__ uint32_t column_mask(int lo, int hi, int sk) {
+  return below(hi + 1) & (~below(lo) | below(sk));
+}
+
 // ---- single rows, exactly --------------------------------------------------------
 // A tile's products multiply masked entries by zero, and 0 x NaN (or 0 x inf) is
 // NaN: a non-finite value of a token that a row does not see can spoil the
@@ -170,14 +178,15 @@ __device__ __noinline__ void fix_dq_row(const SeqParams& p, int b, int h, int i)
   fix_load(g, (const E*)p.dout + (((long long)b * p.S + i) * p.H + h) * p.hd, p.hd);
 #pragma unroll
   for (int t = 0; t < kFixT; ++t) acc[t] = 0.f;
-  const float2 ld = p.ld[((long long)b * p.H + h) * p.ld_stride + i];
+  const long long la = ((long long)b * p.H + h) * p.ld_stride + i;
+  const float nl = p.nl[la], nd = p.nd[la];
   const int lo = max(0, i - p.window + 1);
   for (int j = p.sinks > 0 ? 0 : lo; j <= i; ++j) {
     if (j >= p.sinks && j < lo) j = lo;
     fix_load(x, kb + (long long)j * p.ks, p.hd);
     fix_load(y, vb + (long long)j * p.ks, p.hd);
-    const float w = exp2f(fix_dot(q, x) * p.scale_log2 - ld.x);
-    const float ds = w * (fix_dot(g, y) - ld.y);
+    const float w = exp2f(fix_dot(q, x) * p.scale_log2 + nl);
+    const float ds = w * (fix_dot(g, y) + nd);
 #pragma unroll
     for (int t = 0; t < kFixT; ++t) acc[t] = fmaf(ds, x[t], acc[t]);
   }
@@ -199,9 +208,9 @@ __device__ __noinline__ void fix_dkv_row(const SeqParams& p, const DkvItem& it, 
       if (!seq_visible(p, it.n, i, j)) break;
       fix_load(x, (const E*)p.q + ((long long)it.b * p.S + i) * p.qs + (long long)h * p.hd, p.hd);
       fix_load(y, (const E*)p.dout + (((long long)it.b * p.S + i) * p.H + h) * p.hd, p.hd);
-      const float2 ld = p.ld[((long long)it.b * p.H + h) * p.ld_stride + i];
-      const float w = exp2f(fix_dot(x, k) * p.scale_log2 - ld.x);
-      const float ds = w * (fix_dot(y, v) - ld.y);
+      const long long la = ((long long)it.b * p.H + h) * p.ld_stride + i;
+      const float w = exp2f(fix_dot(x, k) * p.scale_log2 + p.nl[la]);
+      const float ds = w * (fix_dot(y, v) + p.nd[la]);
 #pragma unroll
       for (int t = 0; t < kFixT; ++t) {
         ak[t] = fmaf(ds, x[t], ak[t]);

@@ -260,7 +260,8 @@ __global__ void __launch_bounds__(kThr) gen_dq_kernel(const __grid_constant__ Se
 #pragma unroll
     for (int c = 0; c < NC; ++c) acc[r][c] = 0.f;
     const int i = i0 + ty + 16 * r;
-    ld[r] = i < n ? p.ld[bh * p.ld_stride + i] : make_float2(0.f, 0.f);
+    const long long la = bh * p.ld_stride + i;
+    ld[r] = i < n ? make_float2(p.nl[la], p.nd[la]) : make_float2(0.f, 0.f);
   }
   if (threadIdx.x < T) flags[threadIdx.x] = 0;
   if (i0 < n) {
@@ -286,8 +287,8 @@ __global__ void __launch_bounds__(kThr) gen_dq_kernel(const __grid_constant__ Se
 #pragma unroll
         for (int c = 0; c < R; ++c) {
           const bool see = seq_visible(p, n, i0 + ty + 16 * r, j0 + tx + 16 * c);
-          const float w = exp2f(s[r][c] * p.scale_log2 - ld[r].x);
-          ps[(ty + 16 * r) * (T + 4) + tx + 16 * c] = see ? w * (dp[r][c] - ld[r].y) : 0.f;
+          const float w = exp2f(s[r][c] * p.scale_log2 + ld[r].x);
+          ps[(ty + 16 * r) * (T + 4) + tx + 16 * c] = see ? w * (dp[r][c] + ld[r].y) : 0.f;
         }
       __syncthreads();
       tile_accum<HD, R, T>(acc, ps, ks, ty, tx);
@@ -344,10 +345,11 @@ __global__ void __launch_bounds__(kThr) gen_dkv_kernel(const __grid_constant__ S
                             p.qs, rows, p.hd);
         load_tile<E, HD, T>(gs, (const E*)p.dout + (((long long)it.b * p.S + i0) * p.H + h) * p.hd,
                             (long long)p.H * p.hd, rows, p.hd);
-        if (threadIdx.x < T)
-          lds[threadIdx.x] = (int)threadIdx.x < rows
-                                 ? p.ld[((long long)it.b * p.H + h) * p.ld_stride + i0 + threadIdx.x]
-                                 : make_float2(0.f, 0.f);
+        if (threadIdx.x < T) {
+          const long long la = ((long long)it.b * p.H + h) * p.ld_stride + i0 + threadIdx.x;
+          lds[threadIdx.x] = (int)threadIdx.x < rows ? make_float2(p.nl[la], p.nd[la])
+                                                     : make_float2(0.f, 0.f);
+        }
         __syncthreads();
         float s[R][R], dp[R][R];
         tile_dots<HD, R>(s, ks, qs, ty, tx);
@@ -359,9 +361,9 @@ __global__ void __launch_bounds__(kThr) gen_dkv_kernel(const __grid_constant__ S
             const int i = i0 + tx + 16 * c;
             const float2 ld = lds[tx + 16 * c];
             const bool see = i < it.i1 && seq_visible(p, it.n, i, j0 + ty + 16 * r);
-            const float w = exp2f(s[r][c] * p.scale_log2 - ld.x);
+            const float w = exp2f(s[r][c] * p.scale_log2 + ld.x);
             ps[(ty + 16 * r) * (T + 4) + tx + 16 * c] = see ? w : 0.f;
-            ds[(ty + 16 * r) * (T + 4) + tx + 16 * c] = see ? w * (dp[r][c] - ld.y) : 0.f;
+            ds[(ty + 16 * r) * (T + 4) + tx + 16 * c] = see ? w * (dp[r][c] + ld.y) : 0.f;
           }
         __syncthreads();
         tile_accum<HD, R, T>(av, ps, gs, ty, tx);
@@ -394,23 +396,28 @@ __global__ void __launch_bounds__(kThr) gen_dkv_kernel(const __grid_constant__ S
     if (flags[row] && j0 + row < it.n) fix_dkv_row<E>(p, it, j0 + row);
 }
 
-// (lse * log2 e, D = dO.o) of every row, [B][H][S]: one warp per row, rows of a
-// token side by side so that out and dout are read in order. Bound by HBM
-// (reads out and dout once).
+// (-lse log2 e, -D), D = dO.o, of every row, [B][H][ld_stride]: `lanes` lanes per
+// row (16 bytes of out and dout each at a time), so a warp reads whole lines.
+// Bound by HBM (out and dout once).
 template <typename E>
-__global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ SeqParams p) {
-  const long long row = (long long)blockIdx.x * 8 + threadIdx.x / 32;   // (b S + i) H + h
-  if (row >= (long long)p.B * p.S * p.H) return;
-  const int lane = threadIdx.x & 31;
-  const long long tok = row / p.H;
-  const int h = (int)(row - tok * p.H), b = (int)(tok / p.S), i = (int)(tok - (long long)b * p.S);
+__global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ SeqParams p, int lanes) {
+  const int per = 256 / lanes;
+  const long long row = (long long)blockIdx.x * per + threadIdx.x / lanes;   // (b S + i) H + h
+  const int lane = threadIdx.x % lanes;
+  constexpr int V = 16 / sizeof(E);
   float d = 0.f;
-  const bool real = i < seq_len(p, b);
+  bool real = false;
+  long long at = -1;
+  if (row < (long long)p.B * p.S * p.H) {
+    const long long tok = row / p.H;
+    const int h = (int)(row - tok * p.H), b = (int)(tok / p.S), i = (int)(tok - (long long)b * p.S);
+    at = ((long long)b * p.H + h) * p.ld_stride + i;
+    real = i < seq_len(p, b);
+  }
   if (real) {
     const E* o = (const E*)p.o + row * p.hd;
     const E* g = (const E*)p.dout + row * p.hd;
-    constexpr int V = 16 / sizeof(E);
-    for (int c = lane * V; c < p.hd; c += 32 * V) {
+    for (int c = lane * V; c < p.hd; c += lanes * V) {
       const uint4 uo = *reinterpret_cast<const uint4*>(o + c);
       const uint4 ug = *reinterpret_cast<const uint4*>(g + c);
       const E* eo = reinterpret_cast<const E*>(&uo);
@@ -419,11 +426,11 @@ __global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ SeqPa
       for (int e = 0; e < V; ++e) d = fmaf(seq_ld(eo + e), seq_ld(eg + e), d);
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  if (lane == 0)
-    p.ld[((long long)b * p.H + h) * p.ld_stride + i] =
-        real ? make_float2(p.lse_in[row] * kSeqLog2e, d) : make_float2(INFINITY, 0.f);
+  for (int o = lanes / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  if (lane == 0 && at >= 0) {
+    p.nl[at] = real ? -p.lse_in[row] * kSeqLog2e : -INFINITY;
+    p.nd[at] = -d;
+  }
 }
 
 // dk, dv of every key row whose items left partials, summed in the order of the
@@ -431,16 +438,16 @@ __global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ SeqPa
 template <typename E>
 __global__ void __launch_bounds__(256) dkv_reduce_kernel(const __grid_constant__ SeqParams p) {
   const DkvPlan& d = p.plan;
-  const int q4 = p.hd / 4;
+  const uint32_t q4 = p.hd / 4;
   const long long x = (long long)blockIdx.x * 256 + threadIdx.x;
   // with gs == 1 only the sink tiles have partials
-  const int rows = d.gs > 1 ? p.S : min(p.S, d.nst * d.T);
-  if (x >= (long long)p.B * rows * p.K * q4) return;
-  const int c = (int)(x % q4) * 4;
-  long long y = x / q4;
-  const int kh = (int)(y % p.K);
-  y /= p.K;
-  const int j = (int)(y % rows), b = (int)(y / rows);
+  const uint32_t rows = d.gs > 1 ? p.S : min(p.S, d.nst * d.T);
+  const uint32_t per = p.K * q4;   // of a token
+  const long long tok = x / per;
+  if (tok >= (long long)p.B * rows) return;
+  const uint32_t y = (uint32_t)(x - tok * per);
+  const int kh = y / q4, c = (int)(y - kh * q4) * 4;
+  const int b = (int)((uint32_t)tok / rows), j = (int)((uint32_t)tok - b * rows);
   const int tile = j / d.T;
   float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
   auto add = [](float4& a, const float* s) {
@@ -464,11 +471,16 @@ __global__ void __launch_bounds__(256) dkv_reduce_kernel(const __grid_constant__
     }
   }
   const long long at = ((long long)b * p.S + j) * p.ks + (long long)kh * p.hd + c;
-  const float kk[4] = {k.x, k.y, k.z, k.w}, vv[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    seq_st((E*)p.dk + at + e, kk[e]);
-    seq_st((E*)p.dv + at + e, vv[e]);
+  if constexpr (sizeof(E) == 4) {
+    *reinterpret_cast<float4*>((E*)p.dk + at) = k;
+    *reinterpret_cast<float4*>((E*)p.dv + at) = v;
+  } else {
+    auto pack = [](float4 f) {
+      __nv_bfloat162 h[2] = {__floats2bfloat162_rn(f.x, f.y), __floats2bfloat162_rn(f.z, f.w)};
+      return *reinterpret_cast<uint2*>(h);
+    };
+    *reinterpret_cast<uint2*>((E*)p.dk + at) = pack(k);
+    *reinterpret_cast<uint2*>((E*)p.dv + at) = pack(v);
   }
 }
 
@@ -562,12 +574,14 @@ cudaError_t seq_generic_backward(const SeqParams& p, int dtype, cudaStream_t st)
 }
 
 cudaError_t seq_prep(const SeqParams& p, int dtype, cudaStream_t st) {
-  const long long rows = (long long)p.B * p.S * p.H, grid = (rows + 7) / 8;
+  int lanes = 1;   // 16-byte chunks of a row, as a power of two up to a warp
+  while (lanes < 32 && lanes * (dtype == SWIN_DTYPE_BF16 ? 8 : 4) < p.hd) lanes *= 2;
+  const long long rows = (long long)p.B * p.S * p.H, grid = (rows * lanes + 255) / 256;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   if (dtype == SWIN_DTYPE_BF16)
-    prep_kernel<__nv_bfloat16><<<(unsigned)grid, 256, 0, st>>>(p);
+    prep_kernel<__nv_bfloat16><<<(unsigned)grid, 256, 0, st>>>(p, lanes);
   else
-    prep_kernel<float><<<(unsigned)grid, 256, 0, st>>>(p);
+    prep_kernel<float><<<(unsigned)grid, 256, 0, st>>>(p, lanes);
   note_launch();
   return cudaGetLastError();
 }

@@ -1,0 +1,221 @@
+// seq_tc.cuh -- what the tcgen05 kernels of sequence attention share: bounded
+// waits, rings, the feed of work items, tiles of tokens in shared memory and
+// their matrix descriptors.
+#pragma once
+#include "fast_common.cuh"
+#include "seq_common.cuh"
+
+namespace swin {
+namespace {
+
+// ---- waits -----------------------------------------------------------------------
+// Bounded as mbar_wait is, but the clock is read only after a number of tries (a
+// read costs more than a product's wait usually lasts).
+__device__ __forceinline__ bool seq_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                         int* status) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+  return ptx::mbar_wait(bar, parity, abort, status, kWaitLimitNs);
+}
+// A wait of a whole warp: every lane sees the phase, and all take the same way
+// when the wait is given up.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          int* status) {
+  const bool ok = seq_wait(bar, parity, abort, status);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// True on one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(r));
+  return r != 0;
+}
+// A value that is the same on all lanes, said so that it can live in a uniform
+// register, where tcgen05.mma takes its operands.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Position in a ring of N buffers and the parity of its current round.
+template <int N>
+struct Ring {
+  int s = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == N) {
+      s = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+// ---- work items --------------------------------------------------------------------
+// The grid has one block per item, in order of falling work; a running block
+// takes the next block's place that has not started (cluster launch control)
+// instead of leaving, so items go to whichever SM is free and an item's loads
+// run ahead of the previous one's end. One thread asks (FeedAsk), every role
+// reads the answers (FeedRead) from a ring in shared memory.
+constexpr int kFeed = 4;
+struct Feed {
+  uint4 answer[kFeed];
+  uint64_t full[kFeed], empty[kFeed];
+};
+__device__ __forceinline__ void feed_init(Feed* f, int readers) {
+  for (int i = 0; i < kFeed; ++i) {
+    ptx::mbar_init(&f->full[i], 1);
+    ptx::mbar_init(&f->empty[i], readers);
+  }
+}
+struct FeedAsk {
+  Ring<kFeed> r;
+  Feed* f;
+  uint32_t n = 0;   // questions
+  // Asks for one more item; not again once an answer was "none".
+  __device__ __forceinline__ bool ask(volatile int* abort, int* status) {
+    if (!seq_wait(&f->empty[r.s], r.parity ^ 1, abort, status)) return false;
+    ptx::mbar_arrive_expect_tx(&f->full[r.s], 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+        "[%0], [%1];" ::"r"(ptx::smem_u32(&f->answer[r.s])),
+        "r"(ptx::smem_u32(&f->full[r.s]))
+        : "memory");
+    r.next();
+    ++n;
+    return true;
+  }
+};
+struct FeedRead {
+  Ring<kFeed> r;
+  Feed* f;
+  uint32_t n = 0;   // answers read
+  // The next item into *t; false: there is none (or the wait was given up).
+  // `warp`: all lanes of a warp call together, else one thread alone.
+  template <bool WARP>
+  __device__ __forceinline__ bool next(long long* t, volatile int* abort, int* status) {
+    const bool ok = WARP ? warp_wait(&f->full[r.s], r.parity, abort, status)
+                         : seq_wait(&f->full[r.s], r.parity, abort, status);
+    if (!ok) return false;
+    const uint4 a = f->answer[r.s];
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .b64 lo, hi;\n\t.reg .pred p;\n\t"
+        "mov.b64 lo, {%2, %3};\n\tmov.b64 hi, {%4, %5};\n\t"
+        "mov.b128 h, {lo, hi};\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w));
+    ptx::fence_proxy_async();   // the read comes before the next answer's write
+    if (WARP) __syncwarp();
+    if (!WARP || (threadIdx.x & 31) == 0) ptx::mbar_arrive(&f->empty[r.s]);
+    r.next();
+    ++n;
+    *t = x;
+    return got != 0;
+  }
+};
+
+// An answer still in flight lands before the block leaves (after an abort).
+__device__ __forceinline__ void feed_drain(const FeedAsk& ask, const FeedRead& rd) {
+  if (ask.n > rd.n) ptx::mbar_drain(&rd.f->full[rd.r.s], rd.r.parity, kTestLimitNs * 100);
+}
+
+// ---- tiles -------------------------------------------------------------------------
+// [ROWS tokens][HD] of one head as channel halves of 64: [ROWS][64] regions with
+// the 128-byte swizzle.
+template <int ROWS, int HD>
+__device__ __forceinline__ void load_tokens(const CUtensorMap* m, uint8_t* dst, int h, int row,
+                                            int b, uint64_t* bar) {
+#pragma unroll
+  for (int hf = 0; hf < HD / 64; ++hf)
+    ptx::tma_load_4d(dst + hf * ROWS * 128, m, bar, hf * 64, h, row, b);
+}
+
+// Zeroes rows from .. ROWS - 1 (a warp): what padding tokens hold must not meet a
+// zero weight in a product (0 x NaN).
+template <int ROWS, int HD>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int from) {
+  const int lane = threadIdx.x & 31;
+  for (int hf = 0; hf < HD / 64; ++hf)
+    for (int x = from * 8 + lane; x < ROWS * 8; x += 32)
+      ptx::st_shared_v4(ptx::smem_u32(tile + hf * ROWS * 128 + x * 16), 0u, 0u, 0u, 0u);
+}
+
+// Matrix descriptors are built once per buffer; a K step of 16 then adds a
+// constant (the one issuing thread's instructions are on every step's path).
+__device__ __forceinline__ uint64_t kmajor_base(uint32_t base) {
+  return ptx::smem_desc(base, 16, 1024, ptx::kSwizzle128);
+}
+template <int ROWS>
+__device__ __forceinline__ constexpr uint32_t kmajor_step(int k16) {
+  return ((k16 >> 2) * (ROWS * 128) + (k16 & 3) * 32) >> 4;
+}
+// as MN-major B operand (the channels are N, 16 rows a K step)
+template <int ROWS, int HD>
+__device__ __forceinline__ uint64_t mnmajor_base(uint32_t base) {
+  return ptx::smem_desc(base, HD > 64 ? ROWS * 128 : 1024, 1024, ptx::kSwizzle128);
+}
+__device__ __forceinline__ constexpr uint32_t mnmajor_step(int k16) {
+  return (k16 * 16 * 128) >> 4;
+}
+
+// 32 values as 16 bf16 pairs, rounded; and as the pairs of their top 16 bits with
+// the rest rounded to bf16 in `lo` (x = hi + lo to 2^-16).
+__device__ __forceinline__ void round_pairs(const float* v, uint32_t* w) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) w[e] = ptx::pack_bf16(v[2 * e], v[2 * e + 1]);
+}
+__device__ __forceinline__ void split_pair(float2 v, uint32_t& hi, uint32_t& lo) {
+  const uint32_t a = __float_as_uint(v.x), b = __float_as_uint(v.y);
+  hi = __byte_perm(a, b, 0x7632);
+  lo = ptx::pack_bf16(v.x - __uint_as_float(a & 0xFFFF0000u), v.y - __uint_as_float(b & 0xFFFF0000u));
+}
+// 8 consecutive 32-bit columns into this thread's TMEM lane (warp-collective).
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+// 32 values split into two sets of 16 pairs, to TMEM columns `at` and `at` + 16.
+__device__ __forceinline__ void split_to_columns(uint32_t at, const float* v) {
+#pragma unroll
+  for (int c = 0; c < 32; c += 16) {
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      split_pair(make_float2(v[c + 2 * e], v[c + 2 * e + 1]), hi[e], lo[e]);
+    __syncwarp();
+    tmem_st8u(at + c / 2, hi);
+    tmem_st8u(at + 16 + c / 2, lo);
+  }
+}
+
+// Query rows that see at most this many keys carry P and dS as hi + lo pairs and
+// take D = sum_j P_ij dP_ij from a pass of its own: with few keys an entry's
+// bf16 rounding (2^-8) does not average out, nor does the rounding of the stored
+// o in D = dO.o. The first rows of a sequence are such rows; their errors were
+// 0.04 (o) and 0.11 (gradients) of the tensor's RMS without, where other rows'
+// are at the outputs' own rounding. Costs nothing that shows elsewhere.
+constexpr int kFewKeys = 384;
+
+// The map [hd, heads, S, B] of one operand, box [64, 1, rows, 1].
+inline bool encode_tokens(CUtensorMap* m, const void* base, const SeqParams& p, int heads,
+                          long long stride, int rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.hd, (cuuint64_t)heads, (cuuint64_t)p.S,
+                              (cuuint64_t)p.B};
+  const cuuint64_t strides[3] = {(cuuint64_t)p.hd * 2, (cuuint64_t)stride * 2,
+                                 (cuuint64_t)stride * 2 * p.S};
+  const cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+}  // namespace swin
