@@ -39,7 +39,7 @@ struct SeqParams {
   void *out, *dq, *dk, *dv;
   float* lse;
   float *nl, *nd;                  // backward: -lse log2 e and -D of every row, [B][H][ld_stride]
-  long long ld_stride;             // S rounded up to whole steps of 64 queries
+  long long ld_stride;             // S rounded up to whole tiles of 128 queries
   float *main_part, *sink_part;    // backward partials (see DkvPlan)
   DkvPlan plan;
   int* status;

@@ -67,7 +67,7 @@ SeqParams seq_params(const swin_seqattn_desc* d) {
   p.scale = 1.f / sqrtf((float)d->head_dim);
   p.scale_log2 = kSeqLog2e / sqrtf((float)d->head_dim);
   p.test_timeout = (d->flags & SWIN_FLAG_TEST_TIMEOUT) ? 1 : 0;
-  p.ld_stride = ((long long)d->S + 63) / 64 * 64;
+  p.ld_stride = ((long long)d->S + 127) / 128 * 128;
   p.plan = make_dkv_plan(p.B, p.S, p.K, p.G, p.hd, p.window, p.sinks,
                          seq_fast(d) ? 128 : seq_generic_tile(p.hd));
   return p;

@@ -22,11 +22,12 @@
 // pay two more products per step for an error already below the outputs' own
 // rounding.
 //
-// Warps: 0-15 four softmax warpgroups, two per TMEM buffer, each 32 of the
-// step's 64 columns; 16 the TMA producer; 17 issues S and dP and owns TMEM; 18
-// issues the gradient products. Bound: the tensor pipe (per 128 x 64 step of
-// head_dim 128: S and dP 384 cycles each, limited by shared-memory reads of
-// both operands, 256 for each gradient product).
+// Warps: 0-3 and 4-7 a softmax warpgroup each, taking the steps in turn (thread =
+// row); 8 the TMA producer; 9 issues S and dP and owns TMEM; 10 issues the
+// gradient products. Bound: the tensor pipe at head_dim 128 (per 128 x 64 step S
+// and dP with N = 64, which read both operands from shared memory at 1.5 times
+// the cost of N = 128, and one or two gradient products), the exp unit and the
+// softmax warps' issue slots at 64.
 #include "seq_tc.cuh"
 
 namespace swin {
@@ -35,9 +36,9 @@ namespace {
 using namespace ptx;
 
 constexpr int kStep = 64;         // keys (queries) of a step
-constexpr int kSoft = 16;         // softmax warps
-constexpr int kBProducer = 16, kBMma = 17, kBMma2 = 18;
-constexpr int kBThreads = 19 * 32;
+constexpr int kSoft = 8;          // softmax warps
+constexpr int kBProducer = 8, kBMma = 9, kBMma2 = 10;
+constexpr int kBThreads = 11 * 32;
 // TMEM: NB buffers of S | dP, then ND accumulators of HD columns (dQ) or 2 HD
 // (dV, dK). Three buffers let a step's products start while the two softmax
 // pairs work on those before; head_dim 128 leaves the key side two.
@@ -52,21 +53,6 @@ struct BwdTmem {
 
 struct BwdMaps {
   CUtensorMap a0, a1, b0, b1;   // stationary pair, streamed pair
-};
-
-template <int HD>
-struct BwdCfg {
-  static constexpr uint32_t kTile = kRows * HD * 2;    // stationary tile
-  static constexpr uint32_t kSub = kStep * HD * 2;     // streamed tile
-  static constexpr int kABufs = HD > 64 ? 1 : 2;
-  static constexpr int kStages = HD > 64 ? 4 : 6;
-  static constexpr uint32_t kRing = kABufs * 2 * kTile;
-  static constexpr uint32_t kLd = kRing + kStages * 2 * kSub;
-  static constexpr uint32_t kXch = kLd + kStages * kStep * 8;
-  static constexpr uint32_t kBars = kXch + 4 * kRows * 4;
-  static constexpr uint32_t kFeedAt = kBars + 8 * 40;
-  static constexpr uint32_t kTotal = kFeedAt + sizeof(Feed) + 16;
-  static constexpr uint32_t kSmem = kTotal + 1024;
 };
 
 // An item of either side, for every role alike: `steps` streamed tiles a pass.
@@ -138,6 +124,21 @@ __device__ __forceinline__ BwdItem<KEYS> bwd_item(const SeqParams& p, long long 
   return it;
 }
 
+template <int HD, bool KEYS>
+struct BwdCfg {
+  static constexpr uint32_t kTile = kRows * HD * 2;    // stationary tile
+  static constexpr uint32_t kSub = kStep * HD * 2;     // streamed tile
+  static constexpr int kABufs = HD > 64 ? 1 : 2;
+  static constexpr int kStages = HD > 64 ? 4 : 6;
+  static constexpr uint32_t kRing = kABufs * 2 * kTile;
+  static constexpr uint32_t kLd = kRing + kStages * 2 * kSub;
+  static constexpr uint32_t kXch = kLd + (KEYS ? kStages * kStep : kABufs * kRows) * 8;
+  static constexpr uint32_t kBars = kXch + 2 * kRows * 4;
+  static constexpr uint32_t kFeedAt = kBars + 8 * 40;
+  static constexpr uint32_t kTotal = kFeedAt + sizeof(Feed<BwdItem<KEYS>>) + 16;
+  static constexpr uint32_t kSmem = kTotal + 1024;
+};
+
 // NC fp32 columns of a row times `mul`, zero where !keep, to bf16 rows or fp32
 // partial rows (dst: this lane's row or nullptr); says whether any is not finite.
 template <int NC>
@@ -145,27 +146,27 @@ __device__ __forceinline__ bool store_grad(uint32_t col, float mul, bool keep, v
                                            bool f32) {
   bool bad = false;
 #pragma unroll
-  for (int c = 0; c < NC; c += 16) {
-    float o[16];
+  for (int c = 0; c < NC; c += 32) {
+    float o[32];
     __syncwarp();
-    tmem_ld16(col + c, o);
-    tmem_wait_ld_regs16(o);
-    float big = 0.f;
+    tmem_ld32(col + c, o);
+    tmem_wait_ld_regs(o);
+    float2 odd = make_float2(0.f, 0.f);   // NaN once any entry is not finite
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      big += o[j] * 0.f;                    // NaN once any entry is not finite
-      o[j] = keep ? o[j] * mul : 0.f;
-    }
-    bad |= big != 0.f;
+    for (int j = 0; j < 32; j += 2)
+      odd = __ffma2_rn(make_float2(o[j], o[j + 1]), make_float2(0.f, 0.f), odd);
+    bad |= !(odd.x + odd.y == 0.f);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) o[j] = keep ? o[j] * mul : 0.f;
     if (f32) {
-      uint4 a[4];
+      uint4 a[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 8; ++j)
         a[j] = make_uint4(__float_as_uint(o[4 * j]), __float_as_uint(o[4 * j + 1]),
                           __float_as_uint(o[4 * j + 2]), __float_as_uint(o[4 * j + 3]));
-      store_rows_coalesced<4>(a, dst ? (const void*)((float*)dst + c) : nullptr);
+      store_rows_coalesced<8>(a, dst ? (const void*)((float*)dst + c) : nullptr);
     } else {
-      store_rows_bf16<16>(o, 1.f, dst ? (const void*)((__nv_bfloat16*)dst + c) : nullptr);
+      store_rows_bf16<32>(o, 1.f, dst ? (const void*)((__nv_bfloat16*)dst + c) : nullptr);
     }
   }
   return bad;
@@ -177,13 +178,13 @@ __global__ void __launch_bounds__(kBThreads, 1)
                    const __grid_constant__ BwdMaps maps) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  using C = BwdCfg<HD>;
+  using C = BwdCfg<HD, KEYS>;
   using TM = BwdTmem<HD, KEYS>;
   constexpr int NA = C::kABufs, NS = C::kStages, NB = TM::NB, ND = TM::ND;
   constexpr uint32_t TB = C::kTile, SB = C::kSub;
   uint8_t* abuf = smem;
   uint8_t* ring = smem + C::kRing;
-  float* lds = (float*)(smem + C::kLd);   // per stage: -L of 64 queries, -D
+  float* lds = (float*)(smem + C::kLd);   // -L and -D: of a stage's queries, of a Q tile's
   float* xch = (float*)(smem + C::kXch);
   uint64_t* bars = (uint64_t*)(smem + C::kBars);
   uint64_t* a_full = bars;
@@ -197,26 +198,32 @@ __global__ void __launch_bounds__(kBThreads, 1)
   uint64_t* acc_empty = acc_full + ND;
   uint64_t* drain = acc_empty + ND;   // [2]: one per MMA-issuing thread
   uint64_t* never = drain + 2;
-  Feed* feed = (Feed*)(smem + C::kFeedAt);
-  uint32_t* tmem_slot = (uint32_t*)(smem + C::kFeedAt + sizeof(Feed));
+  using Item = BwdItem<KEYS>;
+  Feed<Item>* feed = (Feed<Item>*)(smem + C::kFeedAt);
+  uint32_t* tmem_slot = (uint32_t*)(smem + C::kFeedAt + sizeof(Feed<Item>));
   volatile int* abort = (volatile int*)(tmem_slot + 1);
   static_assert(2 * NA + 2 * NS + 3 * NB + 2 * ND + 3 <= 40, "barriers");
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NA; ++i) { mbar_init(&a_full[i], 1); mbar_init(&a_empty[i], 1); }
+    // a stationary pair is free once S and dP of its item are done and (query side)
+    // the softmax warps have read its rows' L and D
+    for (int i = 0; i < NA; ++i) {
+      mbar_init(&a_full[i], 1);
+      mbar_init(&a_empty[i], KEYS ? 1 : 1 + kSoft);
+    }
     // a stage is free once the gradient products and (key side) the readers of
     // its (L, D) are done: the latter arrive before p_full, which those wait for
     for (int i = 0; i < NS; ++i) { mbar_init(&b_full[i], 1); mbar_init(&b_empty[i], 1); }
     for (int i = 0; i < NB; ++i) {
-      mbar_init(&s_full[i], 1); mbar_init(&p_full[i], 2 * kWg); mbar_init(&g_done[i], 1);
+      mbar_init(&s_full[i], 1); mbar_init(&p_full[i], kWg); mbar_init(&g_done[i], 1);
     }
     for (int i = 0; i < ND; ++i) {
-      mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4 * kWg);
+      mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 2 * kWg);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
     mbar_init(never, 1);
-    feed_init(feed, 3 + kSoft);   // producer, two MMA warps, the softmax warps
+    feed_init(feed, 2 + kSoft);   // the MMA and softmax warps
     *abort = 0;
     fence_mbar_init();
   }
@@ -234,52 +241,60 @@ __global__ void __launch_bounds__(kBThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  FeedRead rd{{}, feed, 0};
-  long long t = blockIdx.x;
+  FeedRead<Item> rd{feed};
 
   if (warp == kBProducer) {
     if (lane == 0) {
       Ring<NA> ra;
       Ring<NS> rb;
       long long k = 0, e = 0;   // items with work, stages filled
-      FeedAsk ask{{}, feed, 0};
-      bool ok = true;
+      FeedWrite<Item> out{feed};
+      long long t = blockIdx.x;
+      bool ok = true, more = true;
       do {
-        const BwdItem<KEYS> it = bwd_item<KEYS>(p, t);
-        if (!it.steps) continue;
-        uint8_t* a = abuf + ra.s * 2 * TB;
-        uint64_t* af = &a_full[ra.s];
-        if (!seq_wait(&a_empty[ra.s], ra.parity ^ 1, abort, p.status)) break;
-        mbar_arrive_expect_tx(af, 2 * TB);
-        load_tokens<kRows, HD>(&maps.a0, a, it.h, it.r0, it.b, af);
-        load_tokens<kRows, HD>(&maps.a1, a + TB, it.h, it.r0, it.b, af);
-        ra.next();
-        ++k;
-        const int kh = it.h / p.G;
-        for (int ps = 0; ps < it.passes && ok; ++ps) {
-          StepWalk<KEYS> w;
-          for (w.start(it); w.x < it.steps; w.next(it), rb.next(), ++e) {
-            if (!seq_wait(&b_empty[rb.s], rb.parity ^ 1, abort, p.status)) {
-              ok = false;
-              break;
-            }
-            uint64_t* bf = &b_full[rb.s];
-            uint8_t* d = ring + rb.s * 2 * SB;
-            const int h = KEYS ? w.head : kh;
-            mbar_arrive_expect_tx(bf, 2 * SB + (KEYS ? kStep * 8 : 0));
-            load_tokens<kStep, HD>(&maps.b0, d, h, w.row, it.b, bf);
-            load_tokens<kStep, HD>(&maps.b1, d + SB, h, w.row, it.b, bf);
-            if constexpr (KEYS) {   // rows of nl, nd are padded to whole steps
-              const long long at = ((long long)it.b * p.H + h) * p.ld_stride + w.row;
-              bulk_load(lds + rb.s * 2 * kStep, p.nl + at, kStep * 4, bf);
-              bulk_load(lds + rb.s * 2 * kStep + kStep, p.nd + at, kStep * 4, bf);
+        const Item it = bwd_item<KEYS>(p, t);
+        if (!out.put(it, true, abort, p.status)) break;
+        if (it.steps) {
+          uint8_t* a = abuf + ra.s * 2 * TB;
+          uint64_t* af = &a_full[ra.s];
+          if (!seq_wait(&a_empty[ra.s], ra.parity ^ 1, abort, p.status)) break;
+          mbar_arrive_expect_tx(af, 2 * TB + (KEYS ? 0 : kRows * 8));
+          load_tokens<kRows, HD>(&maps.a0, a, it.h, it.r0, it.b, af);
+          load_tokens<kRows, HD>(&maps.a1, a + TB, it.h, it.r0, it.b, af);
+          if constexpr (!KEYS) {   // rows of nl, nd are padded to whole tiles
+            const long long at = ((long long)it.b * p.H + it.h) * p.ld_stride + it.r0;
+            bulk_load(lds + ra.s * 2 * kRows, p.nl + at, kRows * 4, af);
+            bulk_load(lds + ra.s * 2 * kRows + kRows, p.nd + at, kRows * 4, af);
+          }
+          ra.next();
+          ++k;
+          const int kh = it.h / p.G;
+          for (int ps = 0; ps < it.passes && ok; ++ps) {
+            StepWalk<KEYS> w;
+            for (w.start(it); w.x < it.steps; w.next(it), rb.next(), ++e) {
+              if (!seq_wait(&b_empty[rb.s], rb.parity ^ 1, abort, p.status)) {
+                ok = false;
+                break;
+              }
+              uint64_t* bf = &b_full[rb.s];
+              uint8_t* d = ring + rb.s * 2 * SB;
+              const int h = KEYS ? w.head : kh;
+              mbar_arrive_expect_tx(bf, 2 * SB + (KEYS ? kStep * 8 : 0));
+              load_tokens<kStep, HD>(&maps.b0, d, h, w.row, it.b, bf);
+              load_tokens<kStep, HD>(&maps.b1, d + SB, h, w.row, it.b, bf);
+              if constexpr (KEYS) {
+                const long long at = ((long long)it.b * p.H + h) * p.ld_stride + w.row;
+                bulk_load(lds + rb.s * 2 * kStep, p.nl + at, kStep * 4, bf);
+                bulk_load(lds + rb.s * 2 * kStep + kStep, p.nd + at, kStep * 4, bf);
+              }
             }
           }
         }
-        // (asked when the item's loads are out: see seq_fwd_kernel)
-      } while (ok && ask.ask(abort, p.status) && rd.next<false>(&t, abort, p.status));
+        more = ok && out.next(&t, abort, p.status);   // (not earlier: see seq_fwd_kernel)
+      } while (more);
+      if (!*abort) out.put(Item(), false, abort, p.status);
       if (*abort) {
-        feed_drain(ask, rd);
+        out.drain();
         for (long long j = (e > NS ? e - NS : 0); j < e; ++j)
           mbar_drain(&b_full[j % NS], (uint32_t)((j / NS) & 1), kTestLimitNs * 100);
         for (long long j = (k > NA ? k - NA : 0); j < k; ++j)
@@ -295,8 +310,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
     Ring<NB> buf;    // TMEM buffers in turn
     const uint32_t as = smem_u32(abuf), bs = smem_u32(ring);
     bool ok = true;
-    do {
-      const BwdItem<KEYS> it = bwd_item<KEYS>(p, t);
+    while (ok) {
+      const Item* item = rd.next(abort, p.status);
+      if (!item) break;
+      const Item it = *item;
       if (!it.steps) continue;
       if (!warp_wait(&a_full[ra.s], ra.parity, abort, p.status)) break;
       const uint32_t a_at = uniform(as + ra.s * 2 * TB);
@@ -325,7 +342,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
       if (ok && elect_one()) umma_commit(&a_empty[ra.s]);
       __syncwarp();
       ra.next();
-    } while (ok && rd.next<true>(&t, abort, p.status));
+    }
     if (*abort && lane == 0) {
       umma_commit(&drain[0]);
       mbar_drain(&drain[0], 0, kTestLimitNs * 100);
@@ -339,8 +356,10 @@ __global__ void __launch_bounds__(kBThreads, 1)
     Ring<ND> acc;
     const uint32_t bs = smem_u32(ring);
     bool ok = true;
-    do {
-      const BwdItem<KEYS> it = bwd_item<KEYS>(p, t);
+    while (ok) {
+      const Item* item = rd.next(abort, p.status);
+      if (!item) break;
+      const Item it = *item;
       if (!it.steps) continue;
       uint32_t on = 0;   // products add to the accumulators
       for (int ps = 0; ps < it.passes && ok; ++ps) {
@@ -366,14 +385,13 @@ __global__ void __launch_bounds__(kBThreads, 1)
           const bool few = it.few(p, w.row);
           if (elect_one()) {
             if (grads) {
-              // A from TMEM: 16 elements of K are 8 columns; the two column halves
-              // of a step sit 32 columns apart, their low parts 16 behind the high
+              // A from TMEM: 16 elements of K are 8 columns; low parts 32 behind high
 #pragma unroll
               for (int part = 0; part < 2; ++part) {
                 if (part && !few) break;
 #pragma unroll
                 for (int kk = 0; kk < kStep / 16; ++kk) {
-                  const uint32_t a = d + 32 * (kk >> 1) + 8 * (kk & 1) + 16 * part;
+                  const uint32_t a = d + 8 * kk + 32 * part;
                   const uint32_t add = on | (part > 0) | (kk > 0);
                   if constexpr (KEYS) {
                     umma_ts(to, a, b1 + mnmajor_step(kk), idesc, add);
@@ -394,168 +412,175 @@ __global__ void __launch_bounds__(kBThreads, 1)
       if (ok && elect_one()) umma_commit(&acc_full[acc.s]);
       __syncwarp();
       acc.next();
-    } while (ok && rd.next<true>(&t, abort, p.status));
+    }
     if (*abort && lane == 0) {
       umma_commit(&drain[1]);
       mbar_drain(&drain[1], 0, kTestLimitNs * 100);
     }
   } else if (warp < kSoft) {
-    // Warpgroup wg: buffer wg >> 1, columns 32 (wg & 1) .. of its steps; thread =
-    // row (query or key) = TMEM lane.
-    const int wg = warp >> 2, pair = wg >> 1, half = wg & 1;
-    const int row = threadIdx.x & (kWg - 1);
+    // Warpgroup wg takes every second step; thread = row (query or key) = TMEM lane.
+    // Waits name a round of a barrier by its parity; none can be mistaken here:
+    // products are issued in order, and S of step e + NB not before the warpgroup of
+    // step e has written P.
+    const int wg = warp >> 2, row = threadIdx.x & (kWg - 1);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const float c = p.scale_log2;
+    const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
+    Ring<NA> ra;
     Ring<NS> rb;
     Ring<NB> rbuf;
     Ring<ND> racc;
-    uint32_t turn = 0;   // steps so far: the pairs take them in turn
-    bool more = true;
+    uint32_t turn = 0;   // steps so far
     for (;;) {
-      // (barriers are waited for by parity: a pair waits for S of every second step
-      // only, but products are issued in order, and S of step e + NB not before the
-      // pair of step e has written P, so no round can be mistaken for another)
-      // all softmax warps go on together
-      if (named_sync_or(1, kSoft * 32, !more || *abort)) break;
-      const BwdItem<KEYS> it = bwd_item<KEYS>(p, t);
+      const Item* item = rd.next(abort, p.status);
+      // both warpgroups go on together
+      if (named_sync_or(1, kSoft * 32, !item || *abort)) break;
+      const Item& it = *item;
       const int r = it.r0 + row;
       const bool stored = r < p.S, real = r < it.n;
       if (p.test_timeout && it.steps) mbar_wait(never, 0, abort, p.status, kTestLimitNs);
       float nl = 0.f, nd = 0.f;
-      const long long ld_at = ((long long)it.b * p.H + it.h) * p.ld_stride + r;
       if constexpr (!KEYS) {
-        if (real) {
-          nl = p.nl[ld_at];
-          nd = p.nd[ld_at];
+        if (it.steps) {
+          seq_wait(&a_full[ra.s], ra.parity, abort, p.status);
+          nl = lds[ra.s * 2 * kRows + row];
+          nd = lds[ra.s * 2 * kRows + kRows + row];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&a_empty[ra.s]);
+          ra.next();
         }
       }
       float dsum = 0.f;
       StepWalk<KEYS> w;
       if (it.steps) w.start(it);
-      for (int x = 0; x < it.steps * it.passes; ++x, ++turn, w.next(it), rb.next(), rbuf.next()) {
+      const int total = it.steps * it.passes;
+      for (int x = 0; x < total; ++x, ++turn, w.next(it), rb.next(), rbuf.next()) {
         if (!KEYS && x == it.steps) {
           w.start(it);
-          // D of the row: the four warpgroups' parts, in order
+          // D of the row: the two warpgroups' parts, in order
           xch[wg * kRows + row] = dsum;
           named_sync(1, kSoft * 32);
-          nd = -((xch[row] + xch[kRows + row]) + (xch[2 * kRows + row] + xch[3 * kRows + row]));
-          if (wg == 0 && real) p.nd[ld_at] = nd;
+          nd = -(xch[row] + xch[kRows + row]);
+          if (wg == 0 && real) p.nd[((long long)it.b * p.H + it.h) * p.ld_stride + r] = nd;
         }
-        if ((int)(turn & 1) != pair) continue;
-        const uint32_t s_col = tmem + lane_base + rbuf.s * 2 * kStep + 32 * half;
-        const int s = rb.s;
-        const int c0 = w.row + 32 * half;   // first token of these columns
+        if ((int)(turn & 1) != wg) continue;
+        const uint32_t s_col = tmem + lane_base + rbuf.s * 2 * kStep;
+        const int c0 = w.row;   // first token of the step's columns
         seq_wait(&s_full[rbuf.s], rbuf.parity, abort, p.status);
         tc_fence_after();
-        float v[32], g[32];
+        float v[kStep], g[kStep];
         __syncwarp();
         tmem_ld32(s_col, v);
+        tmem_ld32(s_col + 32, v + 32);
         tmem_ld32(s_col + kStep, g);
-        tmem_wait_ld_regs(v);
-        reg_fence32(g);
+        tmem_ld32(s_col + kStep + 32, g + 32);
         // visible columns of the row: lo .. hi, and below sk
         int lo, hi, sk = 0;
         bool plain;
         if constexpr (KEYS) {
           lo = r - c0;
-          const bool sink = r < p.sinks;
-          hi = min(it.d.i1 - 1, sink ? 0x7fffffff : (p.window > 0x7fffffff - r ? 0x7fffffff : r + p.window - 1)) - c0;
-          plain = c0 >= it.r0 + kRows - 1 && c0 + 32 <= it.d.i1 &&
-                  (c0 + 31 - it.r0 < p.window || it.r0 + kRows <= p.sinks);
+          hi = it.d.i1 - 1;
+          if (r >= p.sinks && p.window <= 0x7fffffff - r) hi = min(hi, r + p.window - 1);
+          hi -= c0;
+          plain = c0 >= it.r0 + kRows - 1 && c0 + kStep <= it.d.i1 &&
+                  (c0 + kStep - 1 - it.r0 < p.window || it.r0 + kRows <= p.sinks);
         } else {
           hi = r - c0;
           lo = hi - p.window + 1;
           sk = p.sinks - c0;
-          plain = c0 + 31 <= it.r0 && (it.r0 + kRows - 1 - c0 < p.window || c0 + 32 <= p.sinks);
+          plain = c0 + kStep - 1 <= it.r0 &&
+                  (it.r0 + kRows - 1 - c0 < p.window || c0 + kStep <= p.sinks);
         }
         const bool sums = !KEYS && it.passes == 2 && x < it.steps;   // the pass for D
-        const float2 c2 = make_float2(c, c);
-        const float4* lv = reinterpret_cast<const float4*>(lds + s * 2 * kStep + 32 * half);
+        const float4* lv = reinterpret_cast<const float4*>(lds + rb.s * 2 * kStep);
         const float4* dv = lv + kStep / 4;
         const float sub = sums ? 0.f : nd;
+        const bool few = it.few(p, w.row);
+        tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          float4 l4 = make_float4(nl, nl, nl, nl), d4 = make_float4(sub, sub, sub, sub);
-          if constexpr (KEYS) {   // of four queries
-            l4 = lv[j / 4];
-            d4 = dv[j / 4];
-          }
-          const float2 a = __ffma2_rn(make_float2(v[j], v[j + 1]), c2, make_float2(l4.x, l4.y));
-          const float2 b = __ffma2_rn(make_float2(v[j + 2], v[j + 3]), c2, make_float2(l4.z, l4.w));
-          v[j] = ex2(a.x);
-          v[j + 1] = ex2(a.y);
-          v[j + 2] = ex2(b.x);
-          v[j + 3] = ex2(b.y);
-          const float2 ga = __fmul2_rn(
-              __fadd2_rn(make_float2(g[j], g[j + 1]), make_float2(d4.x, d4.y)),
-              make_float2(v[j], v[j + 1]));
-          const float2 gb = __fmul2_rn(
-              __fadd2_rn(make_float2(g[j + 2], g[j + 3]), make_float2(d4.z, d4.w)),
-              make_float2(v[j + 2], v[j + 3]));
-          g[j] = ga.x;
-          g[j + 1] = ga.y;
-          g[j + 2] = gb.x;
-          g[j + 3] = gb.y;
-        }
-        if (!plain) {
-          const uint32_t see = column_mask(lo, hi, sk);
+        for (int h = 0; h < kStep; h += 32) {
+          // P = 2^(c S - L) and dS = P (dP - D)
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (!(see & (1u << j))) {
-              v[j] = 0.f;
-              g[j] = 0.f;
+          for (int j = h; j < h + 32; j += 4) {
+            float4 l4 = make_float4(nl, nl, nl, nl), d4 = make_float4(sub, sub, sub, sub);
+            if constexpr (KEYS) {   // of four queries
+              l4 = lv[j / 4];
+              d4 = dv[j / 4];
             }
-        }
-        if (sums) {
-          float a0 = 0.f, a1 = 0.f;
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            a0 += g[j];
-            a1 += g[j + 1];
+            const float2 a = __ffma2_rn(make_float2(v[j], v[j + 1]), c2, make_float2(l4.x, l4.y));
+            const float2 b = __ffma2_rn(make_float2(v[j + 2], v[j + 3]), c2, make_float2(l4.z, l4.w));
+            v[j] = ex2(a.x);
+            v[j + 1] = ex2(a.y);
+            v[j + 2] = ex2(b.x);
+            v[j + 3] = ex2(b.y);
+            const float2 ga = __fadd2_rn(make_float2(g[j], g[j + 1]), make_float2(d4.x, d4.y));
+            const float2 gb = __fadd2_rn(make_float2(g[j + 2], g[j + 3]), make_float2(d4.z, d4.w));
+            g[j] = ga.x;
+            g[j + 1] = ga.y;
+            g[j + 2] = gb.x;
+            g[j + 3] = gb.y;
           }
-          dsum += a0 + a1;
-        } else {
-          constexpr int kDs = KEYS ? kStep : 0;   // dS over dP (key side) or S
-          if (it.few(p, w.row)) {
-            if constexpr (KEYS) split_to_columns(s_col, v);
-            split_to_columns(s_col + kDs, g);
+#pragma unroll
+          for (int j = h; j < h + 32; j += 2) {
+            const float2 e = __fmul2_rn(make_float2(g[j], g[j + 1]), make_float2(v[j], v[j + 1]));
+            g[j] = e.x;
+            g[j + 1] = e.y;
+          }
+          if (!plain) {
+            const uint32_t see = column_mask(lo - h, hi - h, sk - h);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(see & (1u << j))) {
+                if constexpr (KEYS) v[h + j] = 0.f;
+                g[h + j] = 0.f;
+              }
+          }
+          if (sums) {
+            float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+            for (int j = h; j < h + 32; j += 2) {
+              a0 += g[j];
+              a1 += g[j + 1];
+            }
+            dsum += a0 + a1;
           } else {
-            uint32_t pk[16];
-            if constexpr (KEYS) {
-              round_pairs(v, pk);
+            const uint32_t s_to = s_col + h / 2, d_to = s_to + (KEYS ? kStep : 0);
+            if (few) {
+              if constexpr (KEYS) split_to_columns(s_to, s_to + 32, v + h);
+              split_to_columns(d_to, d_to + 32, g + h);
+            } else {
+              uint32_t pk[16];
+              if constexpr (KEYS) {
+                round_pairs(v + h, pk);
+                __syncwarp();
+                tmem_st16u(s_to, pk);
+              }
+              round_pairs(g + h, pk);
               __syncwarp();
-              tmem_st16u(s_col, pk);
+              tmem_st16u(d_to, pk);
             }
-            round_pairs(g, pk);
-            __syncwarp();
-            tmem_st16u(s_col + kDs, pk);
           }
-          tmem_wait_st();
         }
+        tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_full[rbuf.s]);
       }
-      // epilogue: each warpgroup a quarter of the accumulator columns
-      constexpr int NC = KEYS ? HD / 2 : HD / 4;
+      // epilogue: a warpgroup stores half of the accumulator columns (dV or dK)
+      constexpr int NC = TM::kAccCols / 2;
       if (it.steps) {
         seq_wait(&acc_full[racc.s], racc.parity, abort, p.status);
         tc_fence_after();
       }
-      // (the item again, rather than kept in registers through the steps)
-      if constexpr (KEYS) asm volatile("" : "+l"(t));
-      const BwdItem<KEYS> at = bwd_item<KEYS>(p, t);
       const uint32_t acc = tmem + lane_base + TM::kAccCol + racc.s * TM::kAccCols + wg * NC;
       void* dst;
       bool f32 = false;
       float mul = p.scale;
       if constexpr (KEYS) {
-        const int off = (wg & 1) * NC;   // dV, dV, dK, dK
-        f32 = at.d.partial;
-        if (f32) dst = (wg < 2 ? at.d.pv : at.d.pk) + row * at.d.row_stride + off;
+        f32 = it.d.partial;
+        if (f32) dst = (wg == 0 ? it.d.pv : it.d.pk) + row * it.d.row_stride;
         else
-          dst = (__nv_bfloat16*)(wg < 2 ? p.dv : p.dk) +
-                ((long long)at.b * p.S + r) * p.ks + (long long)at.h * HD + off;
-        if (wg < 2) mul = 1.f;
+          dst = (__nv_bfloat16*)(wg == 0 ? p.dv : p.dk) +
+                ((long long)it.b * p.S + r) * p.ks + (long long)it.h * HD;
+        if (wg == 0) mul = 1.f;
       } else {
         dst = (__nv_bfloat16*)p.dq + ((long long)it.b * p.S + r) * p.qs + (long long)it.h * HD +
               wg * NC;
@@ -576,12 +601,11 @@ __global__ void __launch_bounds__(kBThreads, 1)
         named_sync(1, kSoft * 32);
         for (int y = warp; y < kRows; y += kSoft)
           if (flags[y]) {
-            if constexpr (KEYS) fix_dkv_row<__nv_bfloat16>(p, at.d, at.r0 + y);
+            if constexpr (KEYS) fix_dkv_row<__nv_bfloat16>(p, it.d, it.r0 + y);
             else fix_dq_row<__nv_bfloat16>(p, it.b, it.h, it.r0 + y);
           }
         named_sync(1, kSoft * 32);
       }
-      more = rd.next<true>(&t, abort, p.status);
     }
   }
   tc_fence_before();
@@ -595,7 +619,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
 template <int HD, bool KEYS>
 cudaError_t bwd_launch(const SeqParams& p, const BwdMaps& maps, cudaStream_t st) {
   auto kernel = seq_bwd_kernel<HD, KEYS>;
-  const int smem = BwdCfg<HD>::kSmem;
+  const int smem = BwdCfg<HD, KEYS>::kSmem;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;

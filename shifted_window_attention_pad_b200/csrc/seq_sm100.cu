@@ -42,25 +42,6 @@ struct SeqMaps {
   CUtensorMap q, k, v;
 };
 
-template <int HD>
-struct SeqFwdCfg {
-  static constexpr int KT = 64;                 // keys of a step
-  static constexpr int NB = HD > 64 ? 2 : 3;    // S buffers of a query tile
-  static constexpr uint32_t kTileCols = NB * KT + HD;  // TMEM columns of a query tile
-  static constexpr uint32_t kOCol = NB * KT;           // O behind the buffers
-  static_assert(2 * kTileCols <= 512, "TMEM columns");
-  static constexpr uint32_t kQTile = kRows * HD * 2;
-  static constexpr uint32_t kSlot = KT * HD * 2;
-  static constexpr int kQBufs = HD > 64 ? 1 : 2;
-  static constexpr int kSlots = HD > 64 ? 8 : 16;       // ring of key / value tiles
-  static constexpr uint32_t kRing = kQBufs * 2 * kQTile;
-  static constexpr uint32_t kBars = kRing + kSlots * kSlot;
-  static constexpr int kNumBars = 2 * kQBufs + 2 * kSlots + 6 * NB + 2 + 2 + 1;
-  static constexpr uint32_t kFeedAt = kBars + (kNumBars * 8 + 15) / 16 * 16;
-  static constexpr uint32_t kTotal = kFeedAt + sizeof(Feed) + 16;
-  static constexpr uint32_t kSmem = kTotal + 1024;
-};
-
 // What an item is, for every role alike.
 template <int KT>
 struct SeqItem {
@@ -98,6 +79,25 @@ __device__ __forceinline__ SeqItem<KT> seq_item(const SeqParams& p, long long t,
 }
 
 template <int HD>
+struct SeqFwdCfg {
+  static constexpr int KT = 64;                 // keys of a step
+  static constexpr int NB = HD > 64 ? 2 : 3;    // S buffers of a query tile
+  static constexpr uint32_t kTileCols = NB * KT + HD;  // TMEM columns of a query tile
+  static constexpr uint32_t kOCol = NB * KT;           // O behind the buffers
+  static_assert(2 * kTileCols <= 512, "TMEM columns");
+  static constexpr uint32_t kQTile = kRows * HD * 2;
+  static constexpr uint32_t kSlot = KT * HD * 2;
+  static constexpr int kQBufs = HD > 64 ? 1 : 2;
+  static constexpr int kSlots = HD > 64 ? 8 : 16;       // ring of key / value tiles
+  static constexpr uint32_t kRing = kQBufs * 2 * kQTile;
+  static constexpr uint32_t kBars = kRing + kSlots * kSlot;
+  static constexpr int kNumBars = 2 * kQBufs + 2 * kSlots + 6 * NB + 2 + 2 + 1;
+  static constexpr uint32_t kFeedAt = kBars + (kNumBars * 8 + 15) / 16 * 16;
+  static constexpr uint32_t kTotal = kFeedAt + sizeof(Feed<SeqItem<KT>>) + 16;
+  static constexpr uint32_t kSmem = kTotal + 1024;
+};
+
+template <int HD>
 __global__ void __launch_bounds__(kSeqThreads, 1)
     seq_fwd_kernel(const __grid_constant__ SeqParams p, const __grid_constant__ SeqMaps maps,
                    const int nq) {
@@ -119,8 +119,9 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
   uint64_t* o_empty = o_done + 2 * NB;   // [2] per query tile: O is read
   uint64_t* drain = o_empty + 2;      // [2]: one per MMA-issuing thread
   uint64_t* never = drain + 2;
-  Feed* feed = (Feed*)(smem + C::kFeedAt);
-  uint32_t* tmem_slot = (uint32_t*)(smem + C::kFeedAt + sizeof(Feed));
+  using Item = SeqItem<KT>;
+  Feed<Item>* feed = (Feed<Item>*)(smem + C::kFeedAt);
+  uint32_t* tmem_slot = (uint32_t*)(smem + C::kFeedAt + sizeof(Feed<Item>));
   volatile int* abort = (volatile int*)(tmem_slot + 1);
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
     }
     for (int i = 0; i < 2; ++i) { mbar_init(&o_empty[i], kWg); mbar_init(&drain[i], 1); }
     mbar_init(never, 1);
-    feed_init(feed, 3 + 8);   // producer, two MMA warps, eight softmax warps
+    feed_init(feed, 2 + 8);   // the MMA and softmax warps
     *abort = 0;
     fence_mbar_init();
   }
@@ -149,18 +150,20 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  FeedRead rd{{}, feed, 0};
-  long long t = blockIdx.x;
+  FeedRead<Item> rd{feed};
 
   if (warp == kSeqProducer) {
     if (lane == 0) {
-      FeedAsk ask{{}, feed, 0};
+      FeedWrite<Item> out{feed};
+      long long t = blockIdx.x;
+      bool more = true;
       Ring<NQ> rq;
       Ring<NS> rs;
       long long k = 0, e = 0;   // items with work, ring slots filled
       bool ok = true;
       do {
-        const SeqItem<KT> it = seq_item<KT>(p, t, nq);
+        const Item it = seq_item<KT>(p, t, nq);
+        if (!out.put(it, true, abort, p.status)) break;
         if (it.steps) {
           const int kh = it.h / p.G;
           if (!seq_wait(&q_empty[rq.s], rq.parity ^ 1, abort, p.status)) break;
@@ -183,13 +186,15 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
         }
         // ask when the item's loads are out, not before: an early question hands
         // the next items out in order, whoever is busy
-      } while (ok && ask.ask(abort, p.status) && rd.next<false>(&t, abort, p.status));
+        more = ok && out.next(&t, abort, p.status);
+      } while (more);
+      if (!*abort) out.put(Item(), false, abort, p.status);
       if (*abort) {  // let copies and answers in flight land before the CTA leaves
         for (long long j = (e > NS ? e - NS : 0); j < e; ++j)
           mbar_drain(&kv_full[j % NS], (uint32_t)((j / NS) & 1), kTestLimitNs * 100);
         for (long long j = (k > NQ ? k - NQ : 0); j < k; ++j)
           mbar_drain(&q_full[j % NQ], (uint32_t)((j / NQ) & 1), kTestLimitNs * 100);
-        feed_drain(ask, rd);
+        out.drain();
       }
     }
   } else if (warp == kSeqMma) {
@@ -201,8 +206,10 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
     Ring<NS> rs;
     Ring<NB> rb[2];   // S buffers of each query tile
     bool ok = true;
-    do {
-      const SeqItem<KT> it = seq_item<KT>(p, t, nq);
+    while (ok) {
+      const Item* item = rd.next(abort, p.status);
+      if (!item) break;
+      const Item it = *item;
       if (!it.steps) continue;
       if (!warp_wait(&q_full[rq.s], rq.parity, abort, p.status)) break;
       for (int x = 0; x < it.steps && ok; ++x) {
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
       if (ok && elect_one()) umma_commit(&q_empty[rq.s]);
       __syncwarp();
       rq.next();
-    } while (ok && rd.next<true>(&t, abort, p.status));
+    }
     if (*abort && lane == 0) {
       umma_commit(&drain[0]);
       mbar_drain(&drain[0], 0, kTestLimitNs * 100);
@@ -250,8 +257,10 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
     Ring<NB> rb[2];
     uint32_t items[2] = {0, 0};   // of a query tile so far
     bool ok = true;
-    do {
-      const SeqItem<KT> it = seq_item<KT>(p, t, nq);
+    while (ok) {
+      const Item* item = rd.next(abort, p.status);
+      if (!item) break;
+      const Item it = *item;
       if (!it.steps) continue;
       uint32_t on[2] = {0, 0};    // products add to O
       for (int x = 0; x < it.steps && ok; ++x) {
@@ -301,7 +310,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
       }
 #pragma unroll
       for (int w = 0; w < 2; ++w) items[w] += it.has[w];
-    } while (ok && rd.next<true>(&t, abort, p.status));
+    }
     if (*abort && lane == 0) {
       umma_commit(&drain[1]);
       mbar_drain(&drain[1], 0, kTestLimitNs * 100);
@@ -317,8 +326,8 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
     // written again.
     uint64_t *sf = s_full + w * NB, *pf = p_full + w * NB, *od = o_done + w * NB;
     Ring<NB> rb, last;   // this product's buffer and the one before's
-    do {
-      const SeqItem<KT> it = seq_item<KT>(p, t, nq);
+    while (const Item* item = rd.next(abort, p.status)) {
+      const Item it = *item;
       const int i0 = it.i0 + w * kRows, i = i0 + row;
       const bool stored = w < nq && i < p.S, real = i < it.n;
       const long long orow = ((long long)it.b * p.S + i) * p.H + it.h;
@@ -469,7 +478,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
         __syncwarp();
         fix_out_row<__nv_bfloat16>(p, it.b, it.h, i0 + (warp & 3) * 32 + r);
       }
-    } while (rd.next<true>(&t, abort, p.status));
+    }
   }
   tc_fence_before();
   __syncthreads();

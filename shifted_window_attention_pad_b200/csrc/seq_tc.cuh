@@ -53,50 +53,55 @@ struct Ring {
 // ---- work items --------------------------------------------------------------------
 // The grid has one block per item, in order of falling work; a running block
 // takes the next block's place that has not started (cluster launch control)
-// instead of leaving, so items go to whichever SM is free and an item's loads
-// run ahead of the previous one's end. One thread asks (FeedAsk), every role
-// reads the answers (FeedRead) from a ring in shared memory.
-constexpr int kFeed = 4;
+// instead of leaving, so items go to whichever SM is free. The producer thread
+// asks, works out what the item is (which takes a look at the lengths: some
+// thousand cycles) and publishes it in a ring that every other role reads, so
+// all of that runs while the roles are busy with the item before.
+constexpr int kFeed = 3;
+template <class Item>
 struct Feed {
-  uint4 answer[kFeed];
-  uint64_t full[kFeed], empty[kFeed];
+  uint4 answer;
+  uint64_t answered, full[kFeed], empty[kFeed];
+  Item item[kFeed];
+  int more[kFeed];
 };
-__device__ __forceinline__ void feed_init(Feed* f, int readers) {
+template <class Item>
+__device__ __forceinline__ void feed_init(Feed<Item>* f, int readers) {
+  ptx::mbar_init(&f->answered, 1);
   for (int i = 0; i < kFeed; ++i) {
     ptx::mbar_init(&f->full[i], 1);
     ptx::mbar_init(&f->empty[i], readers);
   }
 }
-struct FeedAsk {
+// The producer thread's side.
+template <class Item>
+struct FeedWrite {
+  Feed<Item>* f;
   Ring<kFeed> r;
-  Feed* f;
-  uint32_t n = 0;   // questions
-  // Asks for one more item; not again once an answer was "none".
-  __device__ __forceinline__ bool ask(volatile int* abort, int* status) {
+  uint32_t parity = 0;
+  bool open = false;   // a question is out
+  __device__ __forceinline__ bool put(const Item& it, bool more, volatile int* abort, int* status) {
     if (!seq_wait(&f->empty[r.s], r.parity ^ 1, abort, status)) return false;
-    ptx::mbar_arrive_expect_tx(&f->full[r.s], 16);
-    asm volatile(
-        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
-        "[%0], [%1];" ::"r"(ptx::smem_u32(&f->answer[r.s])),
-        "r"(ptx::smem_u32(&f->full[r.s]))
-        : "memory");
+    f->item[r.s] = it;
+    f->more[r.s] = more;
+    ptx::mbar_arrive(&f->full[r.s]);
     r.next();
-    ++n;
     return true;
   }
-};
-struct FeedRead {
-  Ring<kFeed> r;
-  Feed* f;
-  uint32_t n = 0;   // answers read
-  // The next item into *t; false: there is none (or the wait was given up).
-  // `warp`: all lanes of a warp call together, else one thread alone.
-  template <bool WARP>
+  // The next block's place into *t; false: none is left (and none may be asked for
+  // again), or the wait was given up.
   __device__ __forceinline__ bool next(long long* t, volatile int* abort, int* status) {
-    const bool ok = WARP ? warp_wait(&f->full[r.s], r.parity, abort, status)
-                         : seq_wait(&f->full[r.s], r.parity, abort, status);
-    if (!ok) return false;
-    const uint4 a = f->answer[r.s];
+    ptx::mbar_arrive_expect_tx(&f->answered, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+        "[%0], [%1];" ::"r"(ptx::smem_u32(&f->answer)),
+        "r"(ptx::smem_u32(&f->answered))
+        : "memory");
+    open = true;
+    if (!seq_wait(&f->answered, parity, abort, status)) return false;
+    open = false;
+    parity ^= 1;
+    const uint4 a = f->answer;
     uint32_t got, x;
     asm volatile(
         "{\n\t.reg .b128 h;\n\t.reg .b64 lo, hi;\n\t.reg .pred p;\n\t"
@@ -108,19 +113,33 @@ struct FeedRead {
         : "=r"(got), "=r"(x)
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w));
     ptx::fence_proxy_async();   // the read comes before the next answer's write
-    if (WARP) __syncwarp();
-    if (!WARP || (threadIdx.x & 31) == 0) ptx::mbar_arrive(&f->empty[r.s]);
-    r.next();
-    ++n;
     *t = x;
     return got != 0;
   }
+  // An answer still in flight lands before the block leaves (after an abort).
+  __device__ __forceinline__ void drain() {
+    if (open) ptx::mbar_drain(&f->answered, parity, kTestLimitNs * 100);
+  }
 };
-
-// An answer still in flight lands before the block leaves (after an abort).
-__device__ __forceinline__ void feed_drain(const FeedAsk& ask, const FeedRead& rd) {
-  if (ask.n > rd.n) ptx::mbar_drain(&rd.f->full[rd.r.s], rd.r.parity, kTestLimitNs * 100);
-}
+// A role's side (a whole warp calls together). The item stays in shared memory until
+// the role asks for the next one.
+template <class Item>
+struct FeedRead {
+  Feed<Item>* f;
+  Ring<kFeed> r;
+  bool held = false;
+  // The next item, or nullptr at the end.
+  __device__ __forceinline__ const Item* next(volatile int* abort, int* status) {
+    if (held) {
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&f->empty[r.s]);
+      r.next();
+    }
+    held = true;
+    if (!warp_wait(&f->full[r.s], r.parity, abort, status)) return nullptr;
+    return f->more[r.s] ? &f->item[r.s] : nullptr;
+  }
+};
 
 // ---- tiles -------------------------------------------------------------------------
 // [ROWS tokens][HD] of one head as channel halves of 64: [ROWS][64] regions with
@@ -161,8 +180,8 @@ __device__ __forceinline__ constexpr uint32_t mnmajor_step(int k16) {
   return (k16 * 16 * 128) >> 4;
 }
 
-// 32 values as 16 bf16 pairs, rounded; and as the pairs of their top 16 bits with
-// the rest rounded to bf16 in `lo` (x = hi + lo to 2^-16).
+// 32 values as 16 bf16 pairs, rounded; a pair of values as the pair of their top
+// 16 bits and the rest rounded to bf16 (x = hi + lo to 2^-16).
 __device__ __forceinline__ void round_pairs(const float* v, uint32_t* w) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) w[e] = ptx::pack_bf16(v[2 * e], v[2 * e + 1]);
@@ -179,8 +198,8 @@ __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t* r) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
-// 32 values split into two sets of 16 pairs, to TMEM columns `at` and `at` + 16.
-__device__ __forceinline__ void split_to_columns(uint32_t at, const float* v) {
+// 32 values split into two sets of 16 pairs, to TMEM columns `hi_at` and `lo_at`.
+__device__ __forceinline__ void split_to_columns(uint32_t hi_at, uint32_t lo_at, const float* v) {
 #pragma unroll
   for (int c = 0; c < 32; c += 16) {
     uint32_t hi[8], lo[8];
@@ -188,8 +207,8 @@ __device__ __forceinline__ void split_to_columns(uint32_t at, const float* v) {
     for (int e = 0; e < 8; ++e)
       split_pair(make_float2(v[c + 2 * e], v[c + 2 * e + 1]), hi[e], lo[e]);
     __syncwarp();
-    tmem_st8u(at + c / 2, hi);
-    tmem_st8u(at + 16 + c / 2, lo);
+    tmem_st8u(hi_at + c / 2, hi);
+    tmem_st8u(lo_at + c / 2, lo);
   }
 }
 
