@@ -65,7 +65,7 @@ typedef struct swin_seqattn_desc {
   int32_t q_stride, kv_stride;
 } swin_seqattn_desc;
 
-/* Kernel family: 1 = tcgen05/TMA kernels (bf16, head_dim 64 or 128), 0 =
+/* Kernel family: 1 = tcgen05/TMA kernels (bf16, head_dim up to 128), 0 =
  * portable kernels (fp32 and other head sizes). Negative status for an
  * invalid description. Host only. */
 int swin_seqattn_path(const swin_seqattn_desc* desc);

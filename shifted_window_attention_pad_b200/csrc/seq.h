@@ -57,7 +57,7 @@ cudaError_t seq_generic_backward(const SeqParams& p, int dtype, cudaStream_t st)
 cudaError_t seq_prep(const SeqParams& p, int dtype, cudaStream_t st);
 cudaError_t seq_reduce(const SeqParams& p, int dtype, cudaStream_t st);
 
-// tcgen05 / TMA kernels (bf16, head_dim 64 or 128).
+// tcgen05 / TMA kernels (bf16, head_dim up to 128).
 bool seq_fast_supported(int dtype, int hd);
 cudaError_t seq_fast_forward(const SeqParams& p, cudaStream_t st);
 cudaError_t seq_fast_backward(const SeqParams& p, cudaStream_t st);

@@ -1,5 +1,5 @@
 // seq_bwd_sm100.cu -- tcgen05 / TMA backward of sequence attention (bf16,
-// head_dim 64 or 128).
+// head_dim up to 128, in kernels for 64 and 128).
 //
 // Two kernels, because dQ sums over keys and dK, dV over queries, and a sum
 // that crosses blocks would need atomics, whose order changes results:
@@ -139,11 +139,11 @@ struct BwdCfg {
   static constexpr uint32_t kSmem = kTotal + 1024;
 };
 
-// NC fp32 columns of a row times `mul`, zero where !keep, to bf16 rows or fp32
+// NC fp32 columns (the first hd of them) of a row times `mul`, zero where !keep, to bf16 rows or fp32
 // partial rows (dst: this lane's row or nullptr); says whether any is not finite.
 template <int NC>
 __device__ __forceinline__ bool store_grad(uint32_t col, float mul, bool keep, void* dst,
-                                           bool f32) {
+                                           bool f32, int hd) {
   bool bad = false;
 #pragma unroll
   for (int c = 0; c < NC; c += 32) {
@@ -164,9 +164,11 @@ __device__ __forceinline__ bool store_grad(uint32_t col, float mul, bool keep, v
       for (int j = 0; j < 8; ++j)
         a[j] = make_uint4(__float_as_uint(o[4 * j]), __float_as_uint(o[4 * j + 1]),
                           __float_as_uint(o[4 * j + 2]), __float_as_uint(o[4 * j + 3]));
-      store_rows_coalesced<8>(a, dst ? (const void*)((float*)dst + c) : nullptr);
+      store_rows_clipped<8>(a, dst ? (float*)dst + c : nullptr, (hd - c) / 4);
     } else {
-      store_rows_bf16<32>(o, 1.f, dst ? (const void*)((__nv_bfloat16*)dst + c) : nullptr);
+      uint4 a[4];
+      pack_chunks<4>(o, 1.f, a);
+      store_rows_clipped<4>(a, dst ? (__nv_bfloat16*)dst + c : nullptr, (hd - c) / 8);
     }
   }
   return bad;
@@ -579,15 +581,16 @@ __global__ void __launch_bounds__(kBThreads, 1)
         if (f32) dst = (wg == 0 ? it.d.pv : it.d.pk) + row * it.d.row_stride;
         else
           dst = (__nv_bfloat16*)(wg == 0 ? p.dv : p.dk) +
-                ((long long)it.b * p.S + r) * p.ks + (long long)it.h * HD;
+                ((long long)it.b * p.S + r) * p.ks + (long long)it.h * p.hd;
         if (wg == 0) mul = 1.f;
       } else {
-        dst = (__nv_bfloat16*)p.dq + ((long long)it.b * p.S + r) * p.qs + (long long)it.h * HD +
-              wg * NC;
+        dst = (__nv_bfloat16*)p.dq + ((long long)it.b * p.S + r) * p.qs +
+              (long long)it.h * p.hd + wg * NC;
       }
       if (!stored || *abort) dst = nullptr;
       // an item without steps has no products: its rows are zeros whatever TMEM holds
-      const bool bad = store_grad<NC>(acc, mul, real && it.steps, dst, f32) && real && it.steps;
+      const bool bad = store_grad<NC>(acc, mul, real && it.steps, dst, f32,
+                                       p.hd - (KEYS ? 0 : wg * NC)) && real && it.steps;
       if (it.steps) {
         tc_fence_before();
         mbar_arrive(&acc_empty[racc.s]);
@@ -646,9 +649,9 @@ cudaError_t seq_fast_backward(const SeqParams& p, cudaStream_t st) {
       !encode_tokens(&k.b1, p.dout, p, p.H, os, kStep))
     return cudaErrorInvalidValue;
   const cudaError_t e =
-      p.hd == 64 ? bwd_launch<64, false>(p, q, st) : bwd_launch<128, false>(p, q, st);
+      p.hd <= 64 ? bwd_launch<64, false>(p, q, st) : bwd_launch<128, false>(p, q, st);
   if (e != cudaSuccess) return e;
-  return p.hd == 64 ? bwd_launch<64, true>(p, k, st) : bwd_launch<128, true>(p, k, st);
+  return p.hd <= 64 ? bwd_launch<64, true>(p, k, st) : bwd_launch<128, true>(p, k, st);
 }
 
 }  // namespace swin

@@ -1,5 +1,5 @@
 // seq_sm100.cu -- tcgen05 / TMA forward of sequence attention (causal sliding
-// window with sink tokens; bf16, head_dim 64 or 128).
+// window with sink tokens; bf16, head_dim up to 128, in kernels for 64 and 128).
 //
 // One pass over a query tile's visible key tiles with a running maximum and sum.
 // An item is one head's pair of 128-query tiles (or a single tile where pairs
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
       const int i0 = it.i0 + w * kRows, i = i0 + row;
       const bool stored = w < nq && i < p.S, real = i < it.n;
       const long long orow = ((long long)it.b * p.S + i) * p.H + it.h;
-      __nv_bfloat16* dst = (__nv_bfloat16*)p.out + orow * HD;
+      __nv_bfloat16* dst = (__nv_bfloat16*)p.out + orow * p.hd;
       if (p.test_timeout && it.steps) mbar_wait(never, 0, abort, p.status, kTestLimitNs);
       const KeyTiles kt = w ? it.kt[1] : it.kt[0];
       const bool has = w ? it.has[1] : it.has[0], few = w ? it.few(1) : it.few(0);
@@ -433,13 +433,11 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
         rb.next();
       }
       if (!has) {   // padding: zeros
-        float z[64];
-#pragma unroll
-        for (int c = 0; c < 64; ++c) z[c] = 0.f;
         if (w < nq) {
+          uint4 z[8] = {};
 #pragma unroll
           for (int c = 0; c < HD; c += 64)
-            store_rows_bf16<64>(z, 0.f, stored ? (const void*)(dst + c) : nullptr);
+            store_rows_clipped<8>(z, stored ? dst + c : nullptr, (p.hd - c) / 8);
           if (stored && p.lse) p.lse[orow] = 0.f;
         }
         continue;
@@ -467,8 +465,9 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
 #pragma unroll
           for (int j = 0; j < 64; ++j) o[j] = 0.f;
         }
-        store_rows_bf16<64>(o, real ? inv : 0.f,
-                            stored && live ? (const void*)(dst + c) : nullptr);
+        uint4 a[8];
+        pack_chunks<8>(o, real ? inv : 0.f, a);
+        store_rows_clipped<8>(a, stored && live ? dst + c : nullptr, (p.hd - c) / 8);
       }
       if (stored && live && p.lse) p.lse[orow] = real ? (m + __log2f(l)) / kSeqLog2e : 0.f;
       uint32_t fix = __ballot_sync(0xffffffffu, bad && real && live);
@@ -514,11 +513,11 @@ cudaError_t fwd_launch(const SeqParams& p, cudaStream_t st) {
 }  // namespace
 
 bool seq_fast_supported(int dtype, int hd) {
-  return dtype == SWIN_DTYPE_BF16 && (hd == 64 || hd == 128);
+  return dtype == SWIN_DTYPE_BF16 && hd <= 128;
 }
 
 cudaError_t seq_fast_forward(const SeqParams& p, cudaStream_t st) {
-  return p.hd == 64 ? fwd_launch<64>(p, st) : fwd_launch<128>(p, st);
+  return p.hd <= 64 ? fwd_launch<64>(p, st) : fwd_launch<128>(p, st);
 }
 
 }  // namespace swin

@@ -220,7 +220,37 @@ __device__ __forceinline__ void split_to_columns(uint32_t hi_at, uint32_t lo_at,
 // are at the outputs' own rounding. Costs nothing that shows elsewhere.
 constexpr int kFewKeys = 384;
 
-// The map [hd, heads, S, B] of one operand, box [64, 1, rows, 1].
+// Warp-collective store of the warp's 32 rows as store_rows_coalesced does it, with
+// only the first `valid` of the NCH 16-byte chunks written (a head_dim that does
+// not fill the kernel's).
+template <int NCH>
+__device__ __forceinline__ void store_rows_clipped(uint4 (&a)[NCH], void* dst, int valid) {
+  const int lane = threadIdx.x & 31, q = lane & (NCH - 1);
+#pragma unroll
+  for (int d = NCH / 2; d >= 1; d >>= 1) {
+    const bool hi = (q & d) != 0;
+#pragma unroll
+    for (int x = 0; x < NCH; ++x) {
+      if (x & d) continue;
+      uint4 v = hi ? a[x] : a[x + d];   // the chunk that belongs to the other lane
+      v.x = __shfl_xor_sync(0xffffffffu, v.x, d);
+      v.y = __shfl_xor_sync(0xffffffffu, v.y, d);
+      v.z = __shfl_xor_sync(0xffffffffu, v.z, d);
+      v.w = __shfl_xor_sync(0xffffffffu, v.w, d);
+      if (hi) a[x] = v; else a[x + d] = v;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NCH; ++t) {
+    const unsigned long long row =
+        __shfl_sync(0xffffffffu, (unsigned long long)dst, (lane & ~(NCH - 1)) + t);
+    if (row && q < valid)
+      ptx::st_global_v4(reinterpret_cast<uint4*>(row) + q, a[t].x, a[t].y, a[t].z, a[t].w);
+  }
+}
+
+// The map [hd, heads, S, B] of one operand, box [64, 1, rows, 1]; channels beyond hd
+// read as zeros, so the kernels for 64 and 128 channels take every smaller head.
 inline bool encode_tokens(CUtensorMap* m, const void* base, const SeqParams& p, int heads,
                           long long stride, int rows) {
   EncodeTiledFn fn = encode_fn();

@@ -51,7 +51,7 @@ CASES = [
     (1, 2305, 1, 1, 128, 64, 200, None, False),         # two sink tiles in chunks
     (1, 1100, 8, 2, 64, 0, 9, None, False),
     (1, 700, 2, 1, 64, 64, 660, None, False),           # more sinks than windows
-    (2, 200, 4, 2, 80, 50, 3, [200, 150], True),        # head sizes of the portable kernels
+    (2, 200, 4, 2, 80, 50, 3, [200, 150], True),        # heads that do not fill a kernel's
     (1, 150, 2, 2, 8, 0, 0, None, False),
     (1, 130, 2, 1, 256, 33, 2, None, True),
     (2, 90, 2, 2, 136, 20, 0, [90, 64], False),
@@ -72,7 +72,7 @@ def test_against_the_reference(case, dtype):
                 assert not got[name][b, n:].any(), name
 
 
-@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("hd", [8, 40, 64, 72, 128])
 def test_both_kernel_families_agree_with_the_reference(hd):
     q, k, v, g = make(1, 500, 4, 2, hd, "bf16", seed=3)
     want = ref.attention(q, k, v, 200, 4, None, g)
@@ -80,7 +80,7 @@ def test_both_kernel_families_agree_with_the_reference(hd):
         ref.check(run(q, k, v, g, 200, 4, flags=flags), want, ALL)
 
 
-@pytest.mark.parametrize("dtype,hd", [("bf16", 64), ("bf16", 128), ("f32", 64), ("bf16", 80)])
+@pytest.mark.parametrize("dtype,hd", [("bf16", 64), ("bf16", 128), ("f32", 64), ("bf16", 80), ("bf16", 192)])
 def test_large_logits_and_equal_logits(dtype, hd):
     """A running maximum that keeps rising, and rows of equal logits."""
     q, k, v, g = make(1, 400, 2, 2, hd, dtype, seed=5)
@@ -92,7 +92,7 @@ def test_large_logits_and_equal_logits(dtype, hd):
     ref.check(got, ref.attention(zero, k, v, 150, 2, None, g), ALL)
 
 
-@pytest.mark.parametrize("dtype,hd", [("bf16", 64), ("bf16", 128), ("f32", 64), ("bf16", 80)])
+@pytest.mark.parametrize("dtype,hd", [("bf16", 64), ("bf16", 128), ("f32", 64), ("bf16", 80), ("bf16", 192)])
 def test_padding_may_hold_anything(dtype, hd):
     q, k, v, g = make(2, 333, 4, 2, hd, dtype, seed=7)
     lengths = [333, 150]
@@ -103,7 +103,7 @@ def test_padding_may_hold_anything(dtype, hd):
     ref.check(got, want, ALL)
 
 
-@pytest.mark.parametrize("dtype,hd", [("bf16", 64), ("bf16", 128), ("f32", 64), ("bf16", 80)])
+@pytest.mark.parametrize("dtype,hd", [("bf16", 64), ("bf16", 128), ("f32", 64), ("bf16", 80), ("bf16", 192)])
 def test_a_nan_reaches_only_the_rows_that_see_it(dtype, hd):
     """Token 200 of sequence 0 holds NaN: rows that do not see it keep their
     results, those that do are NaN."""

@@ -102,7 +102,7 @@ def test_bad_dtype(L):
 
 
 def test_paths(L):
-    for hd, dtype, want in ((64, "bf16", 1), (128, "bf16", 1), (80, "bf16", 0), (256, "bf16", 0),
+    for hd, dtype, want in ((64, "bf16", 1), (128, "bf16", 1), (80, "bf16", 1), (136, "bf16", 0),
                             (64, "f32", 0)):
         d = sb.make_seq_desc(1, 300, 4, hd, 0, dtype)
         assert sb.swin_seqattn_path(d) == want, (hd, dtype)
