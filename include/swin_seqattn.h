@@ -99,7 +99,8 @@ int swin_seqattn_bwd(const swin_seqattn_desc* desc, const void* q, const void* k
  * B, page_size, num_pages, max_pages >= 1; page_size <= 65536; heads and
  * head_dim as above; window, sinks >= 0. q_stride and kv_stride: elements from
  * one token to the next in q (decode) and in the new keys and values (decode,
- * append); 0 = contiguous. B * kv_heads * max_pages * page_size < 2^40 and
+ * append); 0 = contiguous. At most 1024 query heads to a kv head;
+ * B * kv_heads * max_pages * page_size < 2^40 and
  * max_pages * page_size < 2^31. */
 enum swin_kvcache_flags {
   SWIN_FLAG_KV_WEIGHTS = 1 << 8 /* decode calls will accumulate weights: the workspace also
@@ -120,7 +121,8 @@ typedef struct swin_kvcache_desc {
 int swin_kvcache_workspace_size(const swin_kvcache_desc* desc, size_t* bytes);
 
 /* Writes new tokens into the cache. k, v: [B, T, kv_heads, head_dim], tokens
- * kv_stride elements apart, sequences T tokens apart. `counts` (int32 [B], NULL:
+ * kv_stride elements apart, sequences T tokens apart; T * kv_heads * head_dim
+ * at most 2^31, that times B at most 2^38. `counts` (int32 [B], NULL:
  * T each; clamped to 0 .. T): the first counts[b] tokens of sequence b are
  * written, to positions lengths[b] - counts[b] .. lengths[b] - 1: `lengths`
  * already counts them. A count above the length writes only the tokens whose

@@ -389,67 +389,77 @@ def seq_desc_for(q, k, window, sinks=0, flags=0):
                          k.shape[2], sinks, flags, _token_stride(q), _token_stride(k))
 
 
-class _Call:
-    """Pointers of one call's tensors, all on one device."""
+def _refuse(t, name, dtype, shape, dev):
+    if t is None:
+        raise ValueError("%s is missing" % name)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s is on cuda:%d, the other tensors on cuda:%d"
+                         % (name, t.get_device(), dev))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+    raise ValueError("%s must be contiguous" % name)
 
-    def __init__(self, elem):
-        self.elem, self.device = elem, None
 
-    def _on(self, t, dtype, name):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError("%s must be a CUDA tensor" % name)
-        if t.dtype != dtype:
-            raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, self.device))
+def _device_of(t, name):
+    """Device of a call's first tensor, which the others have to share."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return t.get_device()
 
-    def dense(self, t, shape, name, dtype=None, optional=False):
-        if t is None:
-            if not optional:
-                raise ValueError("%s is missing" % name)
-            return None
-        self._on(t, dtype or self.elem, name)
-        if tuple(t.shape) != shape:
-            raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-        return t.data_ptr()
 
-    def tokens(self, t, shape, stride, name, optional=False):
-        """[B, T, heads, hd] (or [B, heads, hd]) with tokens `stride` elements apart."""
-        if t is None:
-            if not optional:
-                raise ValueError("%s is missing" % name)
-            return None
-        self._on(t, self.elem, name)
-        if tuple(t.shape) != shape:
-            raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-        want = [shape[-1], 1]
-        stride = stride or shape[-2] * shape[-1]
-        want = ([shape[1] * stride, stride] if len(shape) == 4 else [stride]) + want
-        for n, have, need in zip(shape, t.stride(), want):
-            if n > 1 and have != need:
-                raise ValueError("%s has strides %s, the description says %s"
-                                 % (name, t.stride(), tuple(want)))
-        return t.data_ptr()
+def _dense(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor of this type and shape."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape
+            or t.get_device() != dev or not t.is_contiguous()):
+        _refuse(t, name, dtype, shape, dev)
+    return t.data_ptr()
 
-    def run(self, name, workspace, stream, *args):
-        ws = self.dense(workspace, tuple(workspace.shape), "workspace", torch.uint8)
-        dev = self.device
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        elif stream.device != dev:
-            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
-        fn = getattr(lib(), name)
-        if torch.cuda.current_device() == dev.index:
-            rc = fn(*args, ws, workspace.numel(), stream.cuda_stream)
-        else:
-            with torch.cuda.device(dev):
-                rc = fn(*args, ws, workspace.numel(), stream.cuda_stream)
-        if rc != SWIN_OK:
-            raise SwinWattnError(rc, name)
+
+def _maybe(t, name, dtype, shape, dev):
+    return None if t is None else _dense(t, name, dtype, shape, dev)
+
+
+def _tokens(t, name, dtype, shape, stride, dev):
+    """Address of [B, T, heads, hd] or [B, heads, hd] with tokens `stride` elements
+    apart (0: contiguous)."""
+    if not stride:
+        if (isinstance(t, torch.Tensor) and t.shape == shape and not t.is_contiguous()):
+            raise ValueError("%s has strides %s, the description says contiguous"
+                             % (name, t.stride()))
+        return _dense(t, name, dtype, shape, dev)
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape
+            or t.get_device() != dev):
+        _refuse(t, name, dtype, shape, dev)
+    want = (shape[1] * stride, stride) if len(shape) == 4 else (stride,)
+    for n, have, need in zip(shape, t.stride(), want + (shape[-1], 1)):
+        if n > 1 and have != need:
+            raise ValueError("%s has strides %s, the description says %d between tokens"
+                             % (name, t.stride(), stride))
+    return t.data_ptr()
+
+
+def _run(name, fn, dev, workspace, stream, *args):
+    """The call on device `dev` and its current stream (or `stream`)."""
+    if (not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8
+            or workspace.get_device() != dev or not workspace.is_contiguous()):
+        _refuse(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), dev)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)   # current_stream(dev).cuda_stream
+    elif stream.device.index != dev:
+        raise ValueError("the stream is on %s, the tensors on cuda:%d" % (stream.device, dev))
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        rc = fn(*args, workspace.data_ptr(), workspace.numel(), handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, workspace.data_ptr(), workspace.numel(), handle)
+    if rc != SWIN_OK:
+        raise SwinWattnError(rc, name)
 
 
 def swin_seqattn_path(desc):
@@ -491,43 +501,45 @@ def new_cache_workspace(desc, device="cuda"):
 
 
 def _seq_shapes(d):
-    return ((d.B, d.S, d.heads, d.head_dim), (d.B, d.S, d.kv_heads, d.head_dim),
-            (d.B, d.S, d.heads))
+    B, S, H, hd = d.B, d.S, d.heads, d.head_dim
+    return (B, S, H, hd), (B, S, d.kv_heads, hd), (B, S, H)
 
 
 def swin_seqattn_fwd(desc, q, k, v, lengths, out, lse=None, workspace=None, stream=None):
-    c = _Call(_elem(desc))
+    el, dev = _elem(desc), _device_of(q, "q")
     sq, sk, sl = _seq_shapes(desc)
-    args = (c.tokens(q, sq, desc.q_stride, "q"), c.tokens(k, sk, desc.kv_stride, "k"),
-            c.tokens(v, sk, desc.kv_stride, "v"),
-            c.dense(lengths, (desc.B,), "lengths", torch.int32, optional=True),
-            c.dense(out, sq, "out"), c.dense(lse, sl, "lse", torch.float32, optional=True))
+    qs, ks = desc.q_stride, desc.kv_stride
+    args = (_tokens(q, "q", el, sq, qs, dev), _tokens(k, "k", el, sk, ks, dev),
+            _tokens(v, "v", el, sk, ks, dev),
+            _maybe(lengths, "lengths", torch.int32, (desc.B,), dev),
+            _dense(out, "out", el, sq, dev), _maybe(lse, "lse", torch.float32, sl, dev))
     if workspace is None:
-        workspace = new_seq_workspace(desc, c.device)
-    c.run("swin_seqattn_fwd", workspace, stream, ctypes.byref(desc), *args)
+        workspace = new_seq_workspace(desc, q.device)
+    _run("swin_seqattn_fwd", lib().swin_seqattn_fwd, dev, workspace, stream, desc, *args)
     return out
 
 
 def swin_seqattn_bwd(desc, q, k, v, lengths, out, lse, dout, dq, dk, dv, workspace=None,
                      stream=None):
-    c = _Call(_elem(desc))
+    el, dev = _elem(desc), _device_of(q, "q")
     sq, sk, sl = _seq_shapes(desc)
-    args = (c.tokens(q, sq, desc.q_stride, "q"), c.tokens(k, sk, desc.kv_stride, "k"),
-            c.tokens(v, sk, desc.kv_stride, "v"),
-            c.dense(lengths, (desc.B,), "lengths", torch.int32, optional=True),
-            c.dense(out, sq, "out"), c.dense(lse, sl, "lse", torch.float32),
-            c.dense(dout, sq, "dout"), c.tokens(dq, sq, desc.q_stride, "dq"),
-            c.tokens(dk, sk, desc.kv_stride, "dk"), c.tokens(dv, sk, desc.kv_stride, "dv"))
+    qs, ks = desc.q_stride, desc.kv_stride
+    args = (_tokens(q, "q", el, sq, qs, dev), _tokens(k, "k", el, sk, ks, dev),
+            _tokens(v, "v", el, sk, ks, dev),
+            _maybe(lengths, "lengths", torch.int32, (desc.B,), dev),
+            _dense(out, "out", el, sq, dev), _dense(lse, "lse", torch.float32, sl, dev),
+            _dense(dout, "dout", el, sq, dev), _tokens(dq, "dq", el, sq, qs, dev),
+            _tokens(dk, "dk", el, sk, ks, dev), _tokens(dv, "dv", el, sk, ks, dev))
     if workspace is None:
-        workspace = new_seq_workspace(desc, c.device)
-    c.run("swin_seqattn_bwd", workspace, stream, ctypes.byref(desc), *args)
+        workspace = new_seq_workspace(desc, q.device)
+    _run("swin_seqattn_bwd", lib().swin_seqattn_bwd, dev, workspace, stream, desc, *args)
     return dq, dk, dv
 
 
 def seq_forward(desc, q, k, v, lengths=None, want_lse=False, workspace=None):
     sq, _, sl = _seq_shapes(desc)
-    out = torch.empty(sq, dtype=q.dtype, device=q.device)
-    lse = torch.empty(sl, dtype=torch.float32, device=q.device) if want_lse else None
+    out = q.new_empty(sq)
+    lse = q.new_empty(sl, dtype=torch.float32) if want_lse else None
     swin_seqattn_fwd(desc, q, k, v, lengths, out, lse, workspace)
     return (out, lse) if want_lse else out
 
@@ -536,13 +548,13 @@ def seq_backward(desc, q, k, v, out, lse, dout, lengths=None, workspace=None):
     """dq, dk, dv, laid out as the description lays out q, k and v: parts of one
     [B, S, heads + 2 kv_heads, hd] buffer when its strides are that buffer's."""
     B, S, H, K, hd = desc.B, desc.S, desc.heads, desc.kv_heads, desc.head_dim
-    new = lambda n: torch.empty((B, S, n, hd), dtype=q.dtype, device=q.device)
+    new = lambda n: q.new_empty((B, S, n, hd))
     if desc.q_stride and desc.q_stride == desc.kv_stride == (H + 2 * K) * hd:
         both = new(H + 2 * K)
         dq, dk, dv = both[:, :, :H], both[:, :, H:H + K], both[:, :, H + K:]
     else:
-        wide = lambda n, s: (new(n) if not s else torch.empty(
-            (B, S, s), dtype=q.dtype, device=q.device)[:, :, :n * hd].unflatten(2, (n, hd)))
+        wide = lambda n, s: (new(n) if not s else
+                             q.new_empty((B, S, s))[:, :, :n * hd].unflatten(2, (n, hd)))
         dq, dk, dv = wide(H, desc.q_stride), wide(K, desc.kv_stride), wide(K, desc.kv_stride)
     return swin_seqattn_bwd(desc, q, k, v, lengths, out, lse, dout, dq, dk, dv, workspace)
 
@@ -557,61 +569,59 @@ def make_cache_desc(B, heads, head_dim, page_size, num_pages, max_pages, dtype, 
                            kv_stride)
 
 
-def _cache_args(c, d, lengths, page_table, k_cache, v_cache):
+def _cache_args(d, el, dev, lengths, page_table, k_cache, v_cache):
     cache = (d.num_pages, d.kv_heads, d.page_size, d.head_dim)
-    return (c.dense(lengths, (d.B,), "lengths", torch.int32),
-            c.dense(page_table, (d.B, d.max_pages), "page_table", torch.int32),
-            c.dense(k_cache, cache, "k_cache"), c.dense(v_cache, cache, "v_cache"))
-
-
-def _cache_weights(c, d, t, name, optional=True):
-    return c.dense(t, (d.B, d.kv_heads, d.max_pages * d.page_size), name, torch.float32, optional)
+    return (_dense(lengths, "lengths", torch.int32, (d.B,), dev),
+            _dense(page_table, "page_table", torch.int32, (d.B, d.max_pages), dev),
+            _dense(k_cache, "k_cache", el, cache, dev), _dense(v_cache, "v_cache", el, cache, dev))
 
 
 def swin_kvcache_append(desc, k, v, counts, lengths, page_table, k_cache, v_cache,
                         workspace=None, stream=None):
     """k, v: [B, T, kv_heads, head_dim]."""
-    d, c = desc, _Call(_elem(desc))
+    d, el, dev = desc, _elem(desc), _device_of(k, "k")
     T = k.shape[1] if k.dim() == 4 else 0
-    shape = (d.B, T, d.kv_heads, d.head_dim)
-    args = (T, c.tokens(k, shape, d.kv_stride, "k"), c.tokens(v, shape, d.kv_stride, "v"),
-            c.dense(counts, (d.B,), "counts", torch.int32, optional=True),
-            *_cache_args(c, d, lengths, page_table, k_cache, v_cache))
+    shape, ks = (d.B, T, d.kv_heads, d.head_dim), d.kv_stride
+    args = (T, _tokens(k, "k", el, shape, ks, dev), _tokens(v, "v", el, shape, ks, dev),
+            _maybe(counts, "counts", torch.int32, (d.B,), dev),
+            *_cache_args(d, el, dev, lengths, page_table, k_cache, v_cache))
     if workspace is None:
-        workspace = _new_ws(256, c.device)
-    c.run("swin_kvcache_append", workspace, stream, ctypes.byref(d), *args)
+        workspace = _new_ws(256, k.device)
+    _run("swin_kvcache_append", lib().swin_kvcache_append, dev, workspace, stream, d, *args)
 
 
 def swin_kvcache_decode(desc, q, k_new, v_new, lengths, page_table, k_cache, v_cache, weights,
                         new_weights, out, lse=None, workspace=None, stream=None):
-    d, c = desc, _Call(_elem(desc))
-    sk = (d.B, d.kv_heads, d.head_dim)
-    args = (c.tokens(q, (d.B, d.heads, d.head_dim), d.q_stride, "q"),
-            c.tokens(k_new, sk, d.kv_stride, "k_new", optional=True),
-            c.tokens(v_new, sk, d.kv_stride, "v_new", optional=True),
-            *_cache_args(c, d, lengths, page_table, k_cache, v_cache),
-            _cache_weights(c, d, weights, "weights"),
-            _cache_weights(c, d, new_weights, "new_weights"),
-            c.dense(out, (d.B, d.heads, d.head_dim), "out"),
-            c.dense(lse, (d.B, d.heads), "lse", torch.float32, optional=True))
+    d, el, dev = desc, _elem(desc), _device_of(q, "q")
+    B, H = d.B, d.heads
+    so, sk, ks = (B, H, d.head_dim), (B, d.kv_heads, d.head_dim), d.kv_stride
+    sw = (B, d.kv_heads, d.max_pages * d.page_size)
+    args = (_tokens(q, "q", el, so, d.q_stride, dev),
+            None if k_new is None else _tokens(k_new, "k_new", el, sk, ks, dev),
+            None if v_new is None else _tokens(v_new, "v_new", el, sk, ks, dev),
+            *_cache_args(d, el, dev, lengths, page_table, k_cache, v_cache),
+            _maybe(weights, "weights", torch.float32, sw, dev),
+            _maybe(new_weights, "new_weights", torch.float32, sw, dev),
+            _dense(out, "out", el, so, dev), _maybe(lse, "lse", torch.float32, (B, H), dev))
     if workspace is None:
-        workspace = new_cache_workspace(d, c.device)
-    c.run("swin_kvcache_decode", workspace, stream, ctypes.byref(d), *args)
+        workspace = new_cache_workspace(d, q.device)
+    _run("swin_kvcache_decode", lib().swin_kvcache_decode, dev, workspace, stream, d, *args)
     return out
 
 
 def swin_kvcache_evict(desc, weights, lengths, page_table, dst_page_table, k_cache, v_cache,
                        new_weights, new_lengths, kept=None, workspace=None, stream=None):
-    d, c = desc, _Call(_elem(desc))
-    n, t, kc, vc = _cache_args(c, d, lengths, page_table, k_cache, v_cache)
-    args = (_cache_weights(c, d, weights, "weights", False), n, t,
-            c.dense(dst_page_table, (d.B, d.max_pages), "dst_page_table", torch.int32), kc, vc,
-            _cache_weights(c, d, new_weights, "new_weights", False),
-            c.dense(new_lengths, (d.B,), "new_lengths", torch.int32),
-            c.dense(kept, (d.B, d.kv_heads, d.budget), "kept", torch.int32, optional=True))
+    d, el, dev = desc, _elem(desc), _device_of(weights, "weights")
+    sw = (d.B, d.kv_heads, d.max_pages * d.page_size)
+    n, t, kc, vc = _cache_args(d, el, dev, lengths, page_table, k_cache, v_cache)
+    args = (_dense(weights, "weights", torch.float32, sw, dev), n, t,
+            _dense(dst_page_table, "dst_page_table", torch.int32, (d.B, d.max_pages), dev), kc, vc,
+            _dense(new_weights, "new_weights", torch.float32, sw, dev),
+            _dense(new_lengths, "new_lengths", torch.int32, (d.B,), dev),
+            _maybe(kept, "kept", torch.int32, (d.B, d.kv_heads, d.budget), dev))
     if workspace is None:
-        workspace = new_cache_workspace(d, c.device)
-    c.run("swin_kvcache_evict", workspace, stream, ctypes.byref(d), *args)
+        workspace = new_cache_workspace(d, weights.device)
+    _run("swin_kvcache_evict", lib().swin_kvcache_evict, dev, workspace, stream, d, *args)
     return new_weights, new_lengths
 
 
@@ -625,9 +635,8 @@ def cache_decode(desc, q, lengths, page_table, k_cache, v_cache, k_new=None, v_n
                  weights=None, new_weights=None, want_lse=False, workspace=None):
     """Attention of one token per sequence, q [B, heads, hd], over the cache.
     With `weights` and no new_weights the step's weights are added in place."""
-    out = torch.empty((desc.B, desc.heads, desc.head_dim), dtype=q.dtype, device=q.device)
-    lse = (torch.empty((desc.B, desc.heads), dtype=torch.float32, device=q.device)
-           if want_lse else None)
+    out = q.new_empty((desc.B, desc.heads, desc.head_dim))
+    lse = q.new_empty((desc.B, desc.heads), dtype=torch.float32) if want_lse else None
     if weights is not None and new_weights is None:
         new_weights = weights
     swin_kvcache_decode(desc, q, k_new, v_new, lengths, page_table, k_cache, v_cache, weights,

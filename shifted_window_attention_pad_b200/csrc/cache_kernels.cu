@@ -10,7 +10,6 @@ namespace swin {
 namespace {
 
 constexpr int kDecThr = 128;    // decode block: 4 warps
-constexpr int kUnit = 128;      // cache positions of a work unit, 32 per warp
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ int cache_len(const CacheParams& p, int b) {
@@ -32,44 +31,54 @@ __device__ __forceinline__ long long cache_row(const CacheParams& p, const int* 
 }
 
 // ---- append ------------------------------------------------------------------------
-// 16 bytes of one tensor's row per thread, channels fastest: reads and writes
-// whole rows. Bound by HBM (every new row read once and written once).
+// A block takes kAppend x 256 chunks of 16 bytes of one sequence's new rows, channels
+// fastest, four of K and of V in flight per thread. Bound by HBM (every new row
+// read once and written once).
+constexpr int kAppend = 4;
 template <typename E>
-__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ CacheParams p) {
+__global__ void __launch_bounds__(256)
+    append_kernel(const __grid_constant__ CacheParams p, int blocks) {
   constexpr int V = 16 / sizeof(E);
-  const int cpr = p.hd / V;
-  const long long per = (long long)p.T * p.K * cpr;
-  const long long x = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (x >= per * p.B) return;
-  const int b = (int)(x / per);
-  long long y = x - (long long)b * per;
-  const int t = (int)(y / (p.K * cpr));
-  y -= (long long)t * (p.K * cpr);
-  const int kh = (int)(y / cpr), c = (int)(y - (long long)kh * cpr);
+  const int b = blockIdx.x / blocks;   // `blocks` blocks per sequence
+  const uint32_t cpr = p.hd / V, per_tok = p.K * cpr;
   int cnt = p.T;
   if (p.counts) {
     cnt = p.counts[b];
     cnt = cnt < 0 ? 0 : (cnt > p.T ? p.T : cnt);
   }
-  if (t >= cnt) return;
-  const int pos = cache_len(p, b) - cnt + t;
-  if (pos < 0) {
-    atomicExch(p.status, SWIN_ERR_INVALID_ARG);
-    return;
+  const int first = cache_len(p, b) - cnt;
+  const uint32_t x0 = (blockIdx.x - b * blocks) * (256 * kAppend) + threadIdx.x;
+  uint4 k[kAppend], v[kAppend];
+  long long dst[kAppend];
+#pragma unroll
+  for (int u = 0; u < kAppend; ++u) {
+    const uint32_t x = x0 + u * 256;
+    const int t = x / per_tok, y = x - t * per_tok;
+    const int kh = y / cpr, c = (y - kh * cpr) * V;
+    dst[u] = -1;
+    if (t >= cnt) continue;
+    if (first + t < 0) {
+      atomicExch(p.status, SWIN_ERR_INVALID_ARG);
+      continue;
+    }
+    const long long row = cache_row(p, p.table, b, kh, first + t);
+    if (row < 0) continue;
+    const long long src = ((long long)b * p.T + t) * p.ks + (long long)kh * p.hd + c;
+    dst[u] = row * p.hd + c;
+    k[u] = *reinterpret_cast<const uint4*>((const E*)p.k_new + src);
+    v[u] = *reinterpret_cast<const uint4*>((const E*)p.v_new + src);
   }
-  const long long row = cache_row(p, p.table, b, kh, pos);
-  if (row < 0) return;
-  const long long src = ((long long)b * p.T + t) * p.ks + (long long)kh * p.hd + c * V;
-  const long long dst = row * p.hd + c * V;
-  const uint4 k = *reinterpret_cast<const uint4*>((const E*)p.k_new + src);
-  const uint4 v = *reinterpret_cast<const uint4*>((const E*)p.v_new + src);
-  *reinterpret_cast<uint4*>((E*)p.kc + dst) = k;
-  *reinterpret_cast<uint4*>((E*)p.vc + dst) = v;
+#pragma unroll
+  for (int u = 0; u < kAppend; ++u)
+    if (dst[u] >= 0) {
+      *reinterpret_cast<uint4*>((E*)p.kc + dst[u]) = k[u];
+      *reinterpret_cast<uint4*>((E*)p.vc + dst[u]) = v[u];
+    }
 }
 
 // ---- decode ------------------------------------------------------------------------
 // The visible positions of a sequence are numbered 0 .. n - 1: the sinks, then
-// the window (vis_pos). They are cut into units of 128; the units of all
+// the window (vis_pos). They are cut into units of `unit`; the units of all
 // sequences, kv heads and chunks of query heads form one list, and block c of
 // C takes units c T / C .. (c + 1) T / C of the T there are, whatever the mix
 // of lengths: every block gets the same number of bytes to read, which is what
@@ -79,6 +88,7 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ Cac
 // captured graph follows them.
 struct DecodePlan {
   int C, heads, nchunk, hds;     // blocks, query heads of a chunk, chunks, row of partials
+  int unit;                      // visible positions of a work unit
   float* part;                   // [C][2][heads][hds]: m, l (hds - 2, hds - 1) and O
   float* lse2;                   // [B][H] of finished heads, log2 units
   float* logits;                 // weights: [B][H][vis_max], log2 units
@@ -100,17 +110,18 @@ __device__ __forceinline__ Vis vis_of(const CacheParams& p, int b) {
 __device__ __forceinline__ int vis_pos(const Vis& v, int u) {
   return u < v.first ? u : u + v.shift;
 }
-__device__ __forceinline__ int units_of(const CacheParams& p, int b) {
-  return (vis_of(p, b).n + kUnit - 1) / kUnit;
+__device__ __forceinline__ int units_of(const CacheParams& p, int unit, int b) {
+  return (vis_of(p, b).n + unit - 1) / unit;
 }
 
 // Total units per (kv head, chunk) over the batch and, of them, those before
-// sequence `b_stop` (block-wide; kDecThr threads; `sh` holds 10 values).
-__device__ __forceinline__ void batch_units(const CacheParams& p, int b_stop, long long* sh,
-                                            long long& before, long long& total) {
+// sequence `b_stop` (block-wide; THR threads; `sh` holds 2 THR / 32 values).
+template <int THR>
+__device__ __forceinline__ void batch_units(const CacheParams& p, int unit, int b_stop,
+                                            long long* sh, long long& before, long long& total) {
   long long bef = 0, tot = 0;
-  for (int b = threadIdx.x; b < p.B; b += kDecThr) {
-    const int u = units_of(p, b);
+  for (int b = threadIdx.x; b < p.B; b += THR) {
+    const int u = units_of(p, unit, b);
     tot += u;
     if (b < b_stop) bef += u;
   }
@@ -121,22 +132,26 @@ __device__ __forceinline__ void batch_units(const CacheParams& p, int b_stop, lo
   }
   if ((threadIdx.x & 31) == 0) {
     sh[threadIdx.x / 32] = bef;
-    sh[4 + threadIdx.x / 32] = tot;
+    sh[THR / 32 + threadIdx.x / 32] = tot;
   }
   __syncthreads();
-  before = sh[0] + sh[1] + sh[2] + sh[3];
-  total = sh[4] + sh[5] + sh[6] + sh[7];
+  before = total = 0;
+#pragma unroll
+  for (int w = 0; w < THR / 32; ++w) {
+    before += sh[w];
+    total += sh[THR / 32 + w];
+  }
   __syncthreads();
 }
 
 // Sequence that holds the target-th unit of the batch and the units before it.
-__device__ __forceinline__ void find_seq(const CacheParams& p, long long target, long long* sh,
+__device__ __forceinline__ void find_seq(const CacheParams& p, int unit, long long target, long long* sh,
                                          int& b_out, long long& before_out) {
   // each thread a contiguous run of sequences, an exclusive scan over threads
   const int per = (p.B + kDecThr - 1) / kDecThr;
   const int b0 = threadIdx.x * per, b1 = min(p.B, b0 + per);
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += units_of(p, b);
+  for (int b = b0; b < b1; ++b) sum += units_of(p, unit, b);
   long long inc = sum;
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -151,7 +166,7 @@ __device__ __forceinline__ void find_seq(const CacheParams& p, long long target,
   if (target >= before && target < inc) {
     int b = b0;
     for (;;) {
-      const int u = units_of(p, b);
+      const int u = units_of(p, unit, b);
       if (target < before + u) break;
       before += u;
       ++b;
@@ -227,7 +242,7 @@ __device__ __forceinline__ long long lane_row(const CacheParams& p, const Segmen
 // cache is read once, and its bytes bound the kernel.
 template <int HD, int NT, int ST>
 struct MmaCore {
-  static constexpr int kHeads = 8 * NT;
+  static constexpr int kHeads = 8 * NT, kUnit = 128;   // 32 positions per warp
   static constexpr int kCpr = HD / 8;                    // 16-byte chunks of a row
   static constexpr int kTileBytes = 32 * HD * 2;         // one of K, V
   static constexpr int kWarpBytes = ST * 2 * kTileBytes + ST * 4;
@@ -421,13 +436,14 @@ struct MmaCore {
   }
 };
 
-// Any head size and type: lanes across the channels (HT per lane), four
-// positions' rows in flight, up to four query heads. For fp32 its loads keep
-// HBM busy; for narrow bf16 rows with many heads the dot products' shuffles
-// bound it.
+// Any head size and type: lanes across the channels (HT per lane), R positions'
+// rows in flight, up to four query heads. A unit is small (R positions per warp),
+// so that short caches use many SMs. For fp32 its loads keep HBM busy; for narrow
+// bf16 rows with many heads the dot products' shuffles bound it.
 template <typename E, int HT>
 struct LaneCore {
-  static constexpr int kHeads = 4;
+  static constexpr int R = HT <= 2 ? 8 : 4;
+  static constexpr int kHeads = 4, kUnit = 4 * R;   // (decode_shape has the same)
   static constexpr size_t kSmem = 4 * kHeads * (32 * HT + 2) * sizeof(float);
 
   __device__ static void run(const CacheParams& p, const DecodePlan& d, const Segment& s,
@@ -448,63 +464,70 @@ struct LaneCore {
                       : 0.f;
       }
     }
-    const int t_end = min(s.u1 * 4, (s.vis.n + 31) / 32);
-    for (int tile = s.u0 * 4 + warp; tile < t_end; tile += 4) {
-      const long long row = lane_row(p, s, tile * 32 + lane);
-      const int left = min(32, s.vis.n - tile * 32);
+    // runs of R positions: warp, warp + 4, ... of the segment's
+    const int run_end = min(s.u1 * 4, (s.vis.n + R - 1) / R);
+    int run = s.u0 * 4 + warp;
+    auto row_at = [&](int x) {   // lane r < R: position r of run x
+      return lane < R && x < run_end ? lane_row(p, s, x * R + lane) : -1ll;
+    };
+    long long row_next = row_at(run);
 #pragma unroll 1
-      for (int r0 = 0; r0 < left; r0 += 4) {
-        float k[4][HT], v[4][HT];
-        bool ok[4];
+    for (; run < run_end; run += 4) {
+      const long long row = row_next;
+      float k[R][HT], v[R][HT];
+      bool ok[R];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const long long rr = __shfl_sync(0xffffffffu, row, r0 + r);
-          ok[r] = rr != -1;   // positions behind the last are -1 too
-          const E* ks = rr == -2 ? (const E*)p.k_new + new_at : (const E*)p.kc + rr * p.hd;
-          const E* vs = rr == -2 ? (const E*)p.v_new + new_at : (const E*)p.vc + rr * p.hd;
+      for (int r = 0; r < R; ++r) {
+        const long long rr = __shfl_sync(0xffffffffu, row, r);
+        ok[r] = rr != -1;   // positions behind the last are -1 too
+        const E* ks = rr == -2 ? (const E*)p.k_new + new_at : (const E*)p.kc + rr * p.hd;
+        const E* vs = rr == -2 ? (const E*)p.v_new + new_at : (const E*)p.vc + rr * p.hd;
 #pragma unroll
-          for (int t = 0; t < HT; ++t) {
-            const bool in = ok[r] && lane + 32 * t < p.hd;
-            k[r][t] = in ? seq_ld(ks + lane + 32 * t) : 0.f;
-            v[r][t] = in ? seq_ld(vs + lane + 32 * t) : 0.f;
-          }
+        for (int t = 0; t < HT; ++t) {
+          const bool in = ok[r] && lane + 32 * t < p.hd;
+          k[r][t] = in ? seq_ld(ks + lane + 32 * t) : 0.f;
+          v[r][t] = in ? seq_ld(vs + lane + 32 * t) : 0.f;
+        }
+      }
+      row_next = row_at(run + 4);
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h) {
+        if (h >= s.hc) break;
+        float a[R], mx = m[h];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          a[r] = 0.f;
+#pragma unroll
+          for (int t = 0; t < HT; ++t) a[r] = fmaf(q[h][t], k[r][t], a[r]);
         }
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-          if (h >= s.hc) break;
-          float a[4], mx = m[h];
+        for (int w = 16; w > 0; w >>= 1)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            a[r] = 0.f;
+          for (int r = 0; r < R; ++r) a[r] += __shfl_xor_sync(0xffffffffu, a[r], w);
 #pragma unroll
-            for (int t = 0; t < HT; ++t) a[r] = fmaf(q[h][t], k[r][t], a[r]);
-          }
+        for (int r = 0; r < R; ++r) {
+          if (!ok[r]) a[r] = -INFINITY;
+          mx = fmaxf(mx, a[r]);
+        }
+        if (d.logits && lane < R && run * R + lane < s.vis.n) {
+          float x = a[0];
 #pragma unroll
-          for (int w = 16; w > 0; w >>= 1)
+          for (int r = 1; r < R; ++r)
+            if (lane == r) x = a[r];
+          d.logits[((long long)s.b * p.H + s.h0 + h) * d.vis_max + run * R + lane] = x;
+        }
+        const float mu = mx == -INFINITY ? 0.f : mx;
+        const float f = exp2f(m[h] - mu);
+        m[h] = mx;
+        l[h] *= f;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) a[r] += __shfl_xor_sync(0xffffffffu, a[r], w);
+        for (int t = 0; t < HT; ++t) o[h][t] *= f;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            if (!ok[r]) a[r] = -INFINITY;
-            mx = fmaxf(mx, a[r]);
-          }
-          if (d.logits && lane < 4 && r0 + lane < left) {
-            const float x = lane == 0 ? a[0] : (lane == 1 ? a[1] : (lane == 2 ? a[2] : a[3]));
-            d.logits[((long long)s.b * p.H + s.h0 + h) * d.vis_max + tile * 32 + r0 + lane] = x;
-          }
-          const float mu = mx == -INFINITY ? 0.f : mx;
-          const float f = exp2f(m[h] - mu);
-          m[h] = mx;
-          l[h] *= f;
+        for (int r = 0; r < R; ++r) {
+          const float w = exp2f(a[r] - mu);
+          l[h] += w;
 #pragma unroll
-          for (int t = 0; t < HT; ++t) o[h][t] *= f;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float w = exp2f(a[r] - mu);
-            l[h] += w;
-#pragma unroll
-            for (int t = 0; t < HT; ++t) o[h][t] = fmaf(w, v[r][t], o[h][t]);
-          }
+          for (int t = 0; t < HT; ++t) o[h][t] = fmaf(w, v[r][t], o[h][t]);
         }
       }
     }
@@ -534,8 +557,10 @@ __global__ void __launch_bounds__(kDecThr)
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long sh[10];
   float* res = (float*)smem;
+  constexpr int kUnit = Core::kUnit;
+  ptx::grid_dep_launch();   // join_kernel may start (and wait)
   long long dummy, total;
-  batch_units(p, 0, sh, dummy, total);
+  batch_units<kDecThr>(p, kUnit, 0, sh, dummy, total);
   const int kcn = p.K * d.nchunk;
   total *= kcn;
   long long cur = (long long)blockIdx.x * total / d.C;
@@ -543,7 +568,7 @@ __global__ void __launch_bounds__(kDecThr)
   if (cur >= end) return;
   int b;
   long long before;
-  find_seq(p, cur / kcn, sh, b, before);
+  find_seq(p, kUnit, cur / kcn, sh, b, before);
   const int hw = p.hd + 2;
   while (cur < end) {
     Segment s;
@@ -617,81 +642,101 @@ __global__ void __launch_bounds__(kDecThr)
 // Joins the pieces of the heads of (b, kh) that several blocks hold, writes
 // empty sequences, and adds the step's weights: blockIdx.y = piece of
 // kJoinSpan positions (0 also joins). Waits for decode_kernel, whose
-// programmatic dependent it is.
-constexpr int kJoinSpan = 2048;
+// programmatic dependent it is. Per chunk of query heads the pieces' slots are
+// listed once, a warp per head finds the common maximum and sum, and a thread
+// per channel adds the pieces in order.
+constexpr int kJoinSpan = 1024, kJoinThr = 512;
 template <typename E>
-__global__ void __launch_bounds__(kDecThr)
+__global__ void __launch_bounds__(kJoinThr)
     join_kernel(const __grid_constant__ CacheParams p, const __grid_constant__ DecodePlan d) {
-  extern __shared__ float lse_sh[];   // [G]
-  __shared__ long long sh[10];
+  extern __shared__ float join_sh[];
+  float* lse_sh = join_sh;                      // [G]
+  float* inv_sh = lse_sh + p.G;                 // [heads]
+  int* slots = (int*)(inv_sh + d.heads);        // [C]
+  float* fac = (float*)(slots + d.C);           // [heads][C]
+  __shared__ long long sh[2 * kJoinThr / 32];
   const int b = blockIdx.x / p.K, kh = blockIdx.x - b * p.K;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   long long before, total;
-  batch_units(p, b, sh, before, total);
-  ptx::grid_dep_wait();
+  batch_units<kJoinThr>(p, d.unit, b, sh, before, total);
   const int kcn = p.K * d.nchunk;
   total *= kcn;
   const Vis vis = vis_of(p, b);
-  const int U = (vis.n + kUnit - 1) / kUnit;
-  for (int h = threadIdx.x; h < p.G && U == 0; h += kDecThr) lse_sh[h] = -INFINITY;
+  const int U = (vis.n + d.unit - 1) / d.unit;
+  const long long bh0 = (long long)b * p.H + kh * p.G;
+  ptx::grid_dep_wait();
   if (U == 0 && blockIdx.y == 0) {
-    for (int x = threadIdx.x; x < p.G * p.hd; x += kDecThr)
-      seq_st((E*)p.out + ((long long)b * p.H + kh * p.G) * p.hd + x, 0.f);
-    for (int h = threadIdx.x; h < p.G && p.lse; h += kDecThr)
-      p.lse[(long long)b * p.H + kh * p.G + h] = -INFINITY;
+    for (int x = threadIdx.x; x < p.G * p.hd; x += kJoinThr)
+      seq_st((E*)p.out + bh0 * p.hd + x, 0.f);
+    for (int h = threadIdx.x; h < p.G && p.lse; h += kJoinThr) p.lse[bh0 + h] = -INFINITY;
   }
-  if (U > 0)
-    for (int chunk = 0; chunk < d.nchunk; ++chunk) {
-      const long long g0 = (before * p.K * d.nchunk) + ((long long)kh * d.nchunk + chunk) * U;
-      const long long g1 = g0 + U;
-      const int c0 = (int)(((g0 + 1) * d.C - 1) / total), c1 = (int)((g1 * d.C - 1) / total);
-      const int hc = min(d.heads, p.G - chunk * d.heads);
-      const int h0 = chunk * d.heads;   // within the group
-      if (c0 == c1) {
-        for (int h = threadIdx.x; h < hc; h += kDecThr)
-          lse_sh[h0 + h] = d.lse2[(long long)b * p.H + kh * p.G + h0 + h];
-        continue;
+  for (int chunk = 0; chunk < d.nchunk && U > 0; ++chunk) {
+    const long long g0 = before * kcn + ((long long)kh * d.nchunk + chunk) * U, g1 = g0 + U;
+    const int c0 = (int)(((g0 + 1) * d.C - 1) / total), c1 = (int)((g1 * d.C - 1) / total);
+    const int h0 = chunk * d.heads, hc = min(d.heads, p.G - h0);   // within the group
+    if (c0 == c1) {
+      if (p.w_out)
+        for (int h = threadIdx.x; h < hc; h += kJoinThr) lse_sh[h0 + h] = d.lse2[bh0 + h0 + h];
+      continue;
+    }
+    if (blockIdx.y > 0 && !p.w_out) continue;
+    const int ns = c1 - c0 + 1;
+    __syncthreads();
+    for (int k = threadIdx.x; k < ns; k += kJoinThr) {
+      const int c = c0 + k;
+      const long long s0 = c * total / d.C, s1 = (c + 1) * total / d.C;
+      // a block without units has none of this; its first segment is in slot 0
+      slots[k] = max(g0, s0) < min(g1, s1) ? 2 * c + (s0 >= g0 ? 0 : 1) : -1;
+    }
+    __syncthreads();
+    auto piece = [&](int k, int h) {
+      return d.part + ((long long)slots[k] * d.heads + h) * d.hds;
+    };
+    for (int h = warp; h < hc; h += kJoinThr / 32) {
+      float M = -INFINITY, L = 0.f;
+      for (int k = lane; k < ns; k += 32)
+        if (slots[k] >= 0) M = fmaxf(M, piece(k, h)[p.hd]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float mu = M == -INFINITY ? 0.f : M;
+      for (int k = lane; k < ns; k += 32) {
+        float f = 0.f;
+        if (slots[k] >= 0) {
+          f = exp2f(piece(k, h)[p.hd] - mu);
+          L = fmaf(piece(k, h)[p.hd + 1], f, L);
+        }
+        fac[h * d.C + k] = f;
       }
-      auto slot = [&](int c) -> const float* {
-        const long long s0 = c * total / d.C, s1 = (c + 1) * total / d.C;
-        if (max(g0, s0) >= min(g1, s1)) return nullptr;   // a block without units
-        return d.part + ((long long)c * 2 + (s0 >= g0 ? 0 : 1)) * d.heads * d.hds;
-      };
-      for (int x = threadIdx.x; x < hc * p.hd; x += kDecThr) {
-        const int h = x / p.hd, c = x - h * p.hd;
-        if (blockIdx.y > 0 && c > 0) continue;
-        float M = -INFINITY, L = 0.f, O = 0.f;
-        for (int k = c0; k <= c1; ++k) {
-          const float* s = slot(k);
-          if (s) M = fmaxf(M, s[h * d.hds + p.hd]);
-        }
-        const float mu = M == -INFINITY ? 0.f : M;
-        for (int k = c0; k <= c1; ++k) {
-          const float* s = slot(k);
-          if (!s) continue;
-          const float f = exp2f(s[h * d.hds + p.hd] - mu);
-          L = fmaf(s[h * d.hds + p.hd + 1], f, L);
-          O = fmaf(s[h * d.hds + c], f, O);
-        }
-        const long long at = (long long)b * p.H + kh * p.G + h0 + h;
-        if (blockIdx.y == 0) seq_st((E*)p.out + at * p.hd + c, L == 0.f ? 0.f : O / L);
-        if (c == 0) {
-          const float z = lse2_of(M, L);
-          lse_sh[h0 + h] = z;
-          if (p.lse && blockIdx.y == 0) p.lse[at] = z * kLn2;
-        }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      if (lane == 0) {
+        const float z = lse2_of(M, L);
+        lse_sh[h0 + h] = z;
+        inv_sh[h] = L == 0.f ? 0.f : 1.f / L;
+        if (p.lse && blockIdx.y == 0) p.lse[bh0 + h0 + h] = z * kLn2;
       }
     }
+    __syncthreads();
+    for (int x = threadIdx.x; x < hc * p.hd && blockIdx.y == 0; x += kJoinThr) {
+      const int h = x / p.hd, c = x - h * p.hd;
+      float O = 0.f;
+#pragma unroll 8
+      for (int k = 0; k < ns; ++k)
+        if (slots[k] >= 0) O = fmaf(piece(k, h)[c], fac[h * d.C + k], O);
+      seq_st((E*)p.out + (bh0 + h0 + h) * p.hd + c, O * inv_sh[h]);
+    }
+  }
   if (!p.w_out) return;
   __syncthreads();
   const int p1 = (int)min((long long)vis.len, ((long long)blockIdx.y + 1) * kJoinSpan);
   const long long row = ((long long)b * p.K + kh) * p.max_len;
-  for (int pos = blockIdx.y * kJoinSpan + threadIdx.x; pos < p1; pos += kDecThr) {
+  for (int pos = blockIdx.y * kJoinSpan + threadIdx.x; pos < p1; pos += kJoinThr) {
     float w = p.w[row + pos];
-    const bool see = pos < vis.first || pos >= vis.first + vis.shift;
-    if (see) {
+    if (pos < vis.first || pos >= vis.first + vis.shift) {
       const int u = pos < vis.first ? pos : pos - vis.shift;
-      const float* x = d.logits + ((long long)b * p.H + kh * p.G) * d.vis_max + u;
+      const float* x = d.logits + bh0 * d.vis_max + u;
       float sum = 0.f;
+#pragma unroll 8
       for (int h = 0; h < p.G; ++h) {
         const float a = x[h * d.vis_max];   // -inf: a bad page's position
         sum += a == -INFINITY ? 0.f : exp2f(a - lse_sh[h]);
@@ -703,28 +748,78 @@ __global__ void __launch_bounds__(kDecThr)
 }
 
 // ---- evict -------------------------------------------------------------------------
-// Order of weights as unsigned numbers: NaN lowest, then by value, -0 = +0.
+// Order of weights as unsigned numbers, 1 .. 0xff800000: NaN lowest, then by value,
+// -0 = +0. 0 stands for "no position", ~0 for one that always stays.
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  if (w != w) return 0u;
+  if (w != w) return 1u;
   const uint32_t u = __float_as_uint(w + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int kSelThr = 1024;
-constexpr int kSelCache = 40960;   // weights held in shared memory (160 KB)
+constexpr int kSelThr = 1024, kSelRegs = 32;   // positions held in registers: 32 x 1024
 
-// Which positions of (b, kv head) stay: one block each. The threshold is the
-// m-th largest weight of the middle, found bit group by bit group (four
-// passes over 8 bits with a histogram per warp); ties at the threshold are
-// counted off in order of position. Then every warp takes a contiguous run of
-// positions, and two scans over the warps give each its place in the output.
+struct SelectShared {
+  uint32_t hist[32 * 256];   // per warp; then counts in position order
+  uint32_t bin, need, warp_sum[32];
+};
+
+// One digit of the threshold from the block's histograms: the bin that holds the
+// need-th largest key and how many of it are needed.
+__device__ __forceinline__ void pick_bin(SelectShared& sh, uint32_t need) {
+  __syncthreads();
+  if (threadIdx.x < 256) {
+    uint32_t s = 0;
+#pragma unroll
+    for (int v = 0; v < 32; ++v) s += sh.hist[v * 256 + threadIdx.x];
+    sh.hist[threadIdx.x] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {   // bins from the top, eight a lane
+    const int lane = threadIdx.x;
+    uint32_t c[8], sum = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      c[e] = sh.hist[255 - (lane * 8 + e)];
+      sum += c[e];
+    }
+    uint32_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
+    }
+    uint32_t before = inc - sum;
+    if (before < need && need <= inc) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (before < need && need <= before + c[e]) {
+          sh.bin = 255 - (lane * 8 + e);
+          sh.need = need - before;
+          break;
+        }
+        before += c[e];
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// Which positions of (b, kv head) stay: one block each. The always-kept positions
+// have the largest key, so what stays is the `budget` largest keys of the
+// sequence, ties at the threshold in order of position. The threshold is found
+// digit by digit (four passes over 8 bits, a histogram per warp). A kept
+// position's place in the output is the number of larger keys before it plus
+// the ties before it that stay. With R > 0 a thread holds its R positions (1024
+// apart) in registers and one scan over the counts of every warp and round
+// gives all places (n <= 1024 R); R = 0 reads the weights again in every pass
+// and takes a contiguous run of positions per warp. Bound by the passes'
+// instructions: 36 us with the keys in shared memory for 64 x 32768 weights,
+// against the register form's figure in evict_long below.
+template <int R>
 __global__ void __launch_bounds__(kSelThr)
-    evict_select_kernel(const __grid_constant__ CacheParams p, int* kept, int cache_max) {
-  extern __shared__ uint32_t sel[];
-  uint32_t* hist = sel;                 // [32][256]
-  uint32_t* keys = sel + 32 * 256;      // [cache_max]
-  __shared__ uint32_t sh[2];
-  __shared__ int wsum[32];
+    evict_select_kernel(const __grid_constant__ CacheParams p, int* kept) {
+  __shared__ SelectShared sh;
+  ptx::grid_dep_launch();
   const int b = blockIdx.x / p.K, kh = blockIdx.x - b * p.K;
   const int n = cache_len(p, b), keep = min(n, p.budget);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -732,6 +827,16 @@ __global__ void __launch_bounds__(kSelThr)
   float* w_out = p.w_out + ((long long)b * p.K + kh) * p.max_len;
   int* out = kept + ((long long)b * p.K + kh) * p.budget;
   if (kh == 0 && threadIdx.x == 0) p.new_len[b] = keep;
+  const int lo = p.sinks, hi = n - p.recent;       // positions outside stay
+  auto key_of = [&](int x) {
+    return x >= n ? 0u : (x < lo || x >= hi ? 0xffffffffu : weight_key(w[x]));
+  };
+  uint32_t keys[R > 0 ? R : 1];
+  const int rounds = R > 0 ? min(R, (n + kSelThr - 1) / kSelThr) : (n + kSelThr - 1) / kSelThr;
+  if constexpr (R > 0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) keys[r] = r < rounds ? key_of(r * kSelThr + threadIdx.x) : 0u;
+  }
   for (int x = keep + threadIdx.x; x < p.budget; x += kSelThr) out[x] = -1;
   for (long long x = keep + threadIdx.x; x < p.max_len; x += kSelThr) w_out[x] = 0.f;
   if (n <= p.budget) {
@@ -741,153 +846,151 @@ __global__ void __launch_bounds__(kSelThr)
     }
     return;
   }
-  const int lo = p.sinks, hi = n - p.recent;       // the middle
-  const int m = p.budget - p.sinks - p.recent;     // of which m stay, m < hi - lo
-  const bool cached = hi - lo <= cache_max;
-  if (cached)
-    for (int x = lo + threadIdx.x; x < hi; x += kSelThr) keys[x - lo] = weight_key(w[x]);
-  auto key_at = [&](int x) { return cached ? keys[x - lo] : weight_key(w[x]); };
-  uint32_t prefix = 0, thr = 0xffffffffu;
-  int need = m;       // ties at the threshold that stay
-  if (m > 0) {
-    for (int pass = 0; pass < 4; ++pass) {
-      const int sh_bits = 24 - 8 * pass;
-      for (int x = threadIdx.x; x < 32 * 256; x += kSelThr) hist[x] = 0;
-      __syncthreads();
-      for (int x = lo + threadIdx.x; x < hi; x += kSelThr) {
-        const uint32_t k = key_at(x);
-        if (pass == 0 || (k >> (sh_bits + 8)) == prefix)
-          atomicAdd(&hist[warp * 256 + ((k >> sh_bits) & 255)], 1u);
-      }
-      __syncthreads();
-      if (threadIdx.x < 256) {
-        uint32_t s = 0;
+  uint32_t prefix = 0, need = (uint32_t)p.budget;
+#pragma unroll 1
+  for (int pass = 0; pass < 4; ++pass) {
+    const int bits = 24 - 8 * pass;
 #pragma unroll
-        for (int v = 0; v < 32; ++v) s += hist[v * 256 + threadIdx.x];
-        hist[threadIdx.x] = s;
-      }
-      __syncthreads();
-      if (warp == 0) {
-        // bins from the top, eight a lane
-        uint32_t c[8], sum = 0;
+    for (int x = 0; x < 8; ++x) sh.hist[x * kSelThr + threadIdx.x] = 0;
+    __syncthreads();
+    auto count = [&](uint32_t k) {
+      if (k != 0 && (pass == 0 || (k >> (bits + 8)) == prefix))
+        atomicAdd(&sh.hist[warp * 256 + ((k >> bits) & 255)], 1u);
+    };
+    if constexpr (R > 0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          c[e] = hist[255 - (lane * 8 + e)];
-          sum += c[e];
-        }
-        uint32_t inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t t = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += t;
-        }
-        uint32_t before = inc - sum;
-        if (before < (uint32_t)need && (uint32_t)need <= inc) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (before < (uint32_t)need && (uint32_t)need <= before + c[e]) {
-              sh[0] = 255 - (lane * 8 + e);
-              sh[1] = need - before;
-              break;
-            }
-            before += c[e];
-          }
-        }
-      }
-      __syncthreads();
-      prefix = (prefix << 8) | sh[0];
-      need = (int)sh[1];
-      __syncthreads();
+      for (int r = 0; r < R; ++r) count(keys[r]);
+    } else {
+      for (int r = 0; r < rounds; ++r) count(key_of(r * kSelThr + threadIdx.x));
     }
-    thr = prefix;
-  } else {
-    need = 0;
+    pick_bin(sh, need);
+    prefix = (prefix << 8) | sh.bin;
+    need = sh.need;
     __syncthreads();
   }
-  // positions of this warp
-  const int per = ((n + 31) / 32 + 31) / 32 * 32;
-  const int x0 = min(n, warp * per), x1 = min(n, x0 + per);
-  int gt = 0, eq = 0;   // kept outright, ties
-  for (int x = x0 + lane; x < x1; x += 32) {
-    const bool mid = x >= lo && x < hi;
-    const uint32_t k = mid ? key_at(x) : 0u;
-    gt += !mid || (m > 0 && k > thr);
-    eq += mid && m > 0 && k == thr;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    gt += __shfl_xor_sync(0xffffffffu, gt, o);
-    eq += __shfl_xor_sync(0xffffffffu, eq, o);
-  }
-  auto before_warp = [&](int v) {   // sum of v over the warps before this one
-    __syncthreads();
-    if (lane == 0) wsum[warp] = v;
-    __syncthreads();
-    int s = lane < warp ? wsum[lane] : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s;
+  const uint32_t thr = prefix, lt = (1u << lane) - 1u;
+  auto emit = [&](int x, uint32_t k, uint32_t gt_before, uint32_t eq_before) {
+    const uint32_t gt = __ballot_sync(0xffffffffu, k > thr);
+    const uint32_t eq = __ballot_sync(0xffffffffu, k == thr);
+    const uint32_t tie = eq_before + __popc(eq & lt);
+    if (k > thr || (k == thr && tie < need)) {
+      const uint32_t at = gt_before + __popc(gt & lt) + min(tie, need);
+      out[at] = x;
+      w_out[at] = w[x];
+    }
   };
-  int ties = before_warp(eq);                      // ties before this warp's run
-  const int mine = min(max(need - ties, 0), eq);
-  int at = before_warp(gt + mine);
-  for (int x = x0; x < x1; x += 32) {
-    const int y = x + lane;
-    const bool in = y < x1, mid = in && y >= lo && y < hi;
-    const uint32_t k = mid ? key_at(y) : 0u;
-    const bool tie = mid && m > 0 && k == thr;
-    const uint32_t tb = __ballot_sync(0xffffffffu, tie);
-    const int rank = ties + __popc(tb & ((1u << lane) - 1u));
-    const bool stay = in && (!mid || (m > 0 && k > thr) || (tie && rank < need));
-    const uint32_t kb = __ballot_sync(0xffffffffu, stay);
-    if (stay) {
-      const int r = at + __popc(kb & ((1u << lane) - 1u));
-      out[r] = y;
-      w_out[r] = w[y];
+  if constexpr (R > 0) {
+    // larger keys and ties (high half) of every round and warp, in position order
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint32_t gt = __ballot_sync(0xffffffffu, keys[r] > thr);
+      const uint32_t eq = __ballot_sync(0xffffffffu, keys[r] == thr);
+      if (lane == 0) sh.hist[r * 32 + warp] = __popc(gt) | (__popc(eq) << 16);
     }
-    ties += __popc(tb);
-    at += __popc(kb);
+    __syncthreads();
+    const uint32_t c = (int)threadIdx.x < R * 32 ? sh.hist[threadIdx.x] : 0u;
+    uint32_t inc = c;   // both halves at once: each total is at most 32768
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
+    }
+    if (lane == 31) sh.warp_sum[warp] = inc;
+    __syncthreads();
+    uint32_t base = 0;
+    for (int v = 0; v < warp; ++v) base += sh.warp_sum[v];
+    if ((int)threadIdx.x < R * 32) sh.hist[threadIdx.x] = base + inc - c;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r >= rounds) break;
+      const uint32_t before = sh.hist[r * 32 + warp];
+      emit(r * kSelThr + threadIdx.x, keys[r], before & 0xffffu, before >> 16);
+    }
+  } else {
+    const int per = ((n + 31) / 32 + 31) / 32 * 32;   // positions of a warp
+    const int x0 = min(n, warp * per), x1 = min(n, x0 + per);
+    uint32_t gt = 0, eq = 0;
+    for (int x = x0 + lane; x < x1; x += 32) {
+      const uint32_t k = key_of(x);
+      gt += k > thr;
+      eq += k == thr;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      gt += __shfl_xor_sync(0xffffffffu, gt, o);
+      eq += __shfl_xor_sync(0xffffffffu, eq, o);
+    }
+    if (lane == 0) {
+      sh.hist[warp] = gt;
+      sh.hist[32 + warp] = eq;
+    }
+    __syncthreads();
+    gt = eq = 0;
+    for (int v = 0; v < warp; ++v) {
+      gt += sh.hist[v];
+      eq += sh.hist[32 + v];
+    }
+    for (int x = x0; x < x1; x += 32) {
+      const uint32_t k = x + lane < x1 ? key_of(x + lane) : 0u;
+      emit(x + lane, k, gt, eq);
+      gt += __popc(__ballot_sync(0xffffffffu, k > thr));
+      eq += __popc(__ballot_sync(0xffffffffu, k == thr));
+    }
   }
 }
 
-// The kept rows to their new pages, 16 bytes of a K and a V row per thread.
-// Bound by HBM: budget rows read once and written once.
+// The kept rows to their new pages, two chunks of 16 bytes of a K and a V row per
+// thread. Bound by HBM: budget rows read once and written once.
+constexpr int kCopy = 2;
 template <typename E>
 __global__ void __launch_bounds__(256)
     evict_copy_kernel(const __grid_constant__ CacheParams p, const int* kept, int blocks) {
   constexpr int V = 16 / sizeof(E);
   const int cpr = p.hd / V;
-  const int bk = blockIdx.x / blocks;   // `blocks` blocks of 256 chunks per (b, kh)
+  const int bk = blockIdx.x / blocks;   // `blocks` blocks per (b, kh)
   const int b = bk / p.K, kh = bk - b * p.K;
-  const int x = (blockIdx.x - bk * blocks) * 256 + threadIdx.x;
-  const int r = x / cpr, c = x - r * cpr;
+  const int x0 = (blockIdx.x - bk * blocks) * (256 * kCopy) + threadIdx.x;
+  const int keep = min(cache_len(p, b), p.budget);
+  uint4 k[kCopy], v[kCopy];
+  long long dst[kCopy];
   ptx::grid_dep_wait();
-  if (r >= min(cache_len(p, b), p.budget)) return;
-  const int pos = kept[(long long)bk * p.budget + r];
-  const long long src = cache_row(p, p.table, b, kh, pos);
-  const long long dst = cache_row(p, p.dst_table, b, kh, r);
-  if (src < 0 || dst < 0) return;
-  const uint4 k = *reinterpret_cast<const uint4*>((const E*)p.kc + src * p.hd + c * V);
-  const uint4 v = *reinterpret_cast<const uint4*>((const E*)p.vc + src * p.hd + c * V);
-  *reinterpret_cast<uint4*>((E*)p.kc + dst * p.hd + c * V) = k;
-  *reinterpret_cast<uint4*>((E*)p.vc + dst * p.hd + c * V) = v;
+#pragma unroll
+  for (int u = 0; u < kCopy; ++u) {
+    const int x = x0 + u * 256, r = x / cpr, c = (x - r * cpr) * V;
+    dst[u] = -1;
+    if (r >= keep) continue;
+    const long long src = cache_row(p, p.table, b, kh, kept[(long long)bk * p.budget + r]);
+    const long long to = cache_row(p, p.dst_table, b, kh, r);
+    if (src < 0 || to < 0) continue;
+    dst[u] = to * p.hd + c;
+    k[u] = *reinterpret_cast<const uint4*>((const E*)p.kc + src * p.hd + c);
+    v[u] = *reinterpret_cast<const uint4*>((const E*)p.vc + src * p.hd + c);
+  }
+#pragma unroll
+  for (int u = 0; u < kCopy; ++u)
+    if (dst[u] >= 0) {
+      *reinterpret_cast<uint4*>((E*)p.kc + dst[u]) = k[u];
+      *reinterpret_cast<uint4*>((E*)p.vc + dst[u]) = v[u];
+    }
 }
 
 // ---- host --------------------------------------------------------------------------
 struct DecodeShape {
   bool mma;
-  int heads, nchunk, blocks;
+  int heads, nchunk, blocks, unit;
 };
 DecodeShape decode_shape(const CacheParams& p, int dtype) {
   DecodeShape s;
   s.mma = dtype == SWIN_DTYPE_BF16 && (p.hd == 32 || p.hd == 64 || p.hd == 128);
   s.heads = s.mma ? (p.G <= 8 ? 8 : 16) : 4;
   s.nchunk = (p.G + s.heads - 1) / s.heads;
+  s.unit = s.mma ? 128 : (p.hd <= 64 ? 32 : 16);
   // blocks that fit the card at once (shared memory of the ring; registers)
   const long long resident = (long long)kSeqSms * (s.mma ? (p.hd == 128 ? 1 : 2) : 4);
   const long long cap = (long long)p.window + p.sinks;
   const long long vis = p.max_len < cap ? p.max_len : cap;
-  const long long most = (long long)p.B * p.K * s.nchunk * ((vis + kUnit - 1) / kUnit);
+  const long long most = (long long)p.B * p.K * s.nchunk * ((vis + s.unit - 1) / s.unit);
   s.blocks = (int)(most < resident ? most : resident);
   return s;
 }
@@ -920,18 +1023,16 @@ cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cuda
 
 template <typename E, class Core>
 cudaError_t decode_go(const CacheParams& p, const DecodePlan& d, cudaStream_t st) {
-  auto kernel = decode_kernel<E, Core>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)Core::kSmem);
+  cudaError_t e = allow_smem<decode_kernel<E, Core>>(Core::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<d.C, kDecThr, Core::kSmem, st>>>(p, d);
+  decode_kernel<E, Core><<<d.C, kDecThr, Core::kSmem, st>>>(p, d);
   note_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const unsigned pieces = p.w_out ? (unsigned)((p.max_len + kJoinSpan - 1) / kJoinSpan) : 1;
   if (pieces > 65535) return cudaErrorInvalidConfiguration;
-  return launch_dependent(join_kernel<E>, dim3(p.B * p.K, pieces), kDecThr,
-                          (size_t)p.G * sizeof(float), st, p, d);
+  const size_t smem = (size_t)(p.G + d.heads + d.C + d.heads * d.C) * 4;
+  return launch_dependent(join_kernel<E>, dim3(p.B * p.K, pieces), kJoinThr, smem, st, p, d);
 }
 
 template <typename E>
@@ -964,12 +1065,14 @@ size_t cache_workspace(const CacheParams& p, int dtype) {
 
 cudaError_t cache_append(const CacheParams& p, int dtype, cudaStream_t st) {
   const int cpr = p.hd / (dtype == SWIN_DTYPE_BF16 ? 8 : 4);
-  const long long grid = ((long long)p.B * p.T * p.K * cpr + 255) / 256;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const long long blocks = ((long long)p.T * p.K * cpr + 256 * kAppend - 1) / (256 * kAppend);
+  if (blocks * 256 * kAppend > 0x7fffffffLL || blocks * p.B > 0x7fffffffLL)
+    return cudaErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)(blocks * p.B);
   if (dtype == SWIN_DTYPE_BF16)
-    append_kernel<__nv_bfloat16><<<(unsigned)grid, 256, 0, st>>>(p);
+    append_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p, (int)blocks);
   else
-    append_kernel<float><<<(unsigned)grid, 256, 0, st>>>(p);
+    append_kernel<float><<<grid, 256, 0, st>>>(p, (int)blocks);
   note_launch();
   return cudaGetLastError();
 }
@@ -980,6 +1083,7 @@ cudaError_t cache_decode(const CacheParams& p, int dtype, cudaStream_t st) {
   d.C = s.blocks;
   d.heads = s.heads;
   d.nchunk = s.nchunk;
+  d.unit = s.unit;
   d.hds = p.hd + 2;
   d.part = (float*)p.ws;
   d.lse2 = (float*)(p.ws + part_bytes(p, s));
@@ -994,17 +1098,19 @@ cudaError_t cache_evict(const CacheParams& p, int dtype, cudaStream_t st) {
   int* kept = p.kept ? p.kept : (int*)p.ws;
   const long long bk = (long long)p.B * p.K;
   if (bk > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const int cache_max = (int)(p.max_len < kSelCache ? p.max_len : kSelCache);
-  const size_t smem = 32 * 256 * 4 + (size_t)cache_max * 4;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  evict_select_kernel<<<(unsigned)bk, kSelThr, smem, st>>>(p, kept, cache_max);
+  // registers for the positions a sequence can have; beyond 32768 the form without
+  if (p.max_len <= 4 * kSelThr)
+    evict_select_kernel<4><<<(unsigned)bk, kSelThr, 0, st>>>(p, kept);
+  else if (p.max_len <= kSelRegs * kSelThr)
+    evict_select_kernel<kSelRegs><<<(unsigned)bk, kSelThr, 0, st>>>(p, kept);
+  else
+    evict_select_kernel<0><<<(unsigned)bk, kSelThr, 0, st>>>(p, kept);
   note_launch();
-  e = cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int cpr = p.hd / (dtype == SWIN_DTYPE_BF16 ? 8 : 4);
-  const long long blocks = ((long long)p.budget * cpr + 255) / 256, grid = blocks * bk;
+  const long long per = 256 * kCopy;
+  const long long blocks = ((long long)p.budget * cpr + per - 1) / per, grid = blocks * bk;
   if ((long long)p.budget * cpr > 0x7fffff00LL || grid > 0x7fffffffLL)
     return cudaErrorInvalidConfiguration;
   return dtype == SWIN_DTYPE_BF16

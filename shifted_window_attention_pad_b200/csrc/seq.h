@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/swin_seqattn.h"
 #include "kernels.h"
 
@@ -28,6 +30,19 @@ struct DkvPlan {
   long long items;                 // B * K * gs * (nst * qc + ntiles - nst)
   size_t main_bytes, sink_bytes;   // partials of dk and dv together
 };
+
+// Lets `Kernel` use `bytes` of dynamic shared memory, once per device.
+template <auto Kernel>
+cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};   // by device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
 
 struct SeqParams {
   int B, S, H, K, G, hd;

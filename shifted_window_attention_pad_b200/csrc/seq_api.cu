@@ -108,7 +108,8 @@ int check_cache(const swin_kvcache_desc* d) {
     return SWIN_ERR_INVALID_ARG;
   const long long len = (long long)d->max_pages * d->page_size;
   if (len > 0x7fffffffLL || len * d->B > (1LL << 40) / d->kv_heads) return SWIN_ERR_INVALID_ARG;
-  if ((long long)d->B * d->heads > 0x7fffffffLL) return SWIN_ERR_INVALID_ARG;
+  if (d->heads / d->kv_heads > 1024 || (long long)d->B * d->heads > 0x7fffffffLL)
+    return SWIN_ERR_INVALID_ARG;
   // evict's own fields are checked by that call; here only that they can size a workspace
   if (d->budget < 0 || d->budget > len || d->recent < 0) return SWIN_ERR_INVALID_ARG;
   return SWIN_OK;
@@ -229,7 +230,8 @@ int swin_kvcache_append(const swin_kvcache_desc* desc, int32_t T, const void* k,
   rc = check_ws(workspace, workspace_bytes, kWsHeader);
   if (rc) return rc;
   CacheParams p = cache_params(desc);
-  if ((long long)T * p.B * p.K * p.hd > (1LL << 40)) return SWIN_ERR_INVALID_ARG;
+  if ((long long)T * p.K * p.hd > (1LL << 31) || (long long)T * p.B * p.K * p.hd > (1LL << 38))
+    return SWIN_ERR_INVALID_ARG;
   p.status = (int*)workspace;
   p.T = T; p.k_new = k; p.v_new = v; p.counts = counts; p.lengths = lengths; p.table = page_table;
   p.kc = k_cache; p.vc = v_cache;

@@ -621,15 +621,14 @@ __global__ void __launch_bounds__(kBThreads, 1)
 
 template <int HD, bool KEYS>
 cudaError_t bwd_launch(const SeqParams& p, const BwdMaps& maps, cudaStream_t st) {
-  auto kernel = seq_bwd_kernel<HD, KEYS>;
-  const int smem = BwdCfg<HD, KEYS>::kSmem;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  using C = BwdCfg<HD, KEYS>;
+  static_assert(C::kSmem <= kSmemLimit, "shared memory");
+  const cudaError_t e = allow_smem<seq_bwd_kernel<HD, KEYS>>(C::kSmem);
   if (e != cudaSuccess) return e;
   const long long items =
       KEYS ? p.plan.items : (long long)p.B * p.H * ((p.S + kRows - 1) / kRows);
   if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  kernel<<<(unsigned)items, kBThreads, smem, st>>>(p, maps);
+  seq_bwd_kernel<HD, KEYS><<<(unsigned)items, kBThreads, C::kSmem, st>>>(p, maps);
   note_launch();
   return cudaGetLastError();
 }

@@ -495,17 +495,15 @@ cudaError_t fwd_launch(const SeqParams& p, cudaStream_t st) {
       !encode_tokens(&maps.k, p.k, p, p.K, p.ks, C::KT) ||
       !encode_tokens(&maps.v, p.v, p, p.K, p.ks, C::KT))
     return cudaErrorInvalidValue;
-  auto kernel = seq_fwd_kernel<HD>;
   static_assert(C::kSmem <= kSmemLimit, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)C::kSmem);
+  const cudaError_t e = allow_smem<seq_fwd_kernel<HD>>(C::kSmem);
   if (e != cudaSuccess) return e;
   // pairs of query tiles, unless they leave more than half of the SMs idle
   const long long tiles = (p.S + kRows - 1) / kRows, bh = (long long)p.B * p.H;
-  const int nq = tiles > 1 && (tiles + 1) / 2 * bh > num_sms() / 2 ? 2 : 1;
+  const int nq = tiles > 1 && (tiles + 1) / 2 * bh > kSeqSms / 2 ? 2 : 1;
   const long long items = (tiles + nq - 1) / nq * bh;
   if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  kernel<<<(unsigned)items, kSeqThreads, C::kSmem, st>>>(p, maps, nq);
+  seq_fwd_kernel<HD><<<(unsigned)items, kSeqThreads, C::kSmem, st>>>(p, maps, nq);
   note_launch();
   return cudaGetLastError();
 }
