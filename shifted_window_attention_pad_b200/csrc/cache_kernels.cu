@@ -144,10 +144,16 @@ __device__ __forceinline__ void batch_units(const CacheParams& p, int unit, int 
   __syncthreads();
 }
 
-// Sequence that holds the target-th unit of the batch and the units before it.
-__device__ __forceinline__ void find_seq(const CacheParams& p, int unit, long long target, long long* sh,
-                                         int& b_out, long long& before_out) {
-  // each thread a contiguous run of sequences, an exclusive scan over threads
+// The block's place in the list of units: total units of the batch (per kv head and
+// chunk), and the sequence that holds unit `start / kcn` of block c's first unit
+// with the units before it. One pass over the lengths: each thread a contiguous run
+// of sequences, an exclusive scan over threads (`sh` holds 7 values).
+struct Place {
+  long long total, start, end, before;
+  int b;
+};
+__device__ __forceinline__ Place find_place(const CacheParams& p, int unit, int C, int kcn,
+                                            long long* sh) {
   const int per = (p.B + kDecThr - 1) / kDecThr;
   const int b0 = threadIdx.x * per, b1 = min(p.B, b0 + per);
   long long sum = 0;
@@ -161,9 +167,19 @@ __device__ __forceinline__ void find_seq(const CacheParams& p, int unit, long lo
   }
   if (lane == 31) sh[threadIdx.x / 32] = inc;
   __syncthreads();
-  for (int w = 0; w < (int)threadIdx.x / 32; ++w) inc += sh[w];
+  Place pl;
+  pl.total = 0;
+#pragma unroll
+  for (int w = 0; w < kDecThr / 32; ++w) {
+    if (w < (int)threadIdx.x / 32) inc += sh[w];
+    pl.total += sh[w];
+  }
+  pl.total *= kcn;
+  pl.start = (long long)blockIdx.x * pl.total / C;
+  pl.end = (long long)(blockIdx.x + 1) * pl.total / C;
+  const long long target = pl.start / kcn;
   long long before = inc - sum;
-  if (target >= before && target < inc) {
+  if (pl.start < pl.end && target >= before && target < inc) {
     int b = b0;
     for (;;) {
       const int u = units_of(p, unit, b);
@@ -171,13 +187,13 @@ __device__ __forceinline__ void find_seq(const CacheParams& p, int unit, long lo
       before += u;
       ++b;
     }
-    sh[8] = b;
-    sh[9] = before;
+    sh[5] = b;
+    sh[6] = before;
   }
   __syncthreads();
-  b_out = (int)sh[8];
-  before_out = sh[9];
-  __syncthreads();
+  pl.b = (int)sh[5];
+  pl.before = sh[6];
+  return pl;
 }
 
 struct Segment {
@@ -555,21 +571,16 @@ template <typename E, class Core>
 __global__ void __launch_bounds__(kDecThr)
     decode_kernel(const __grid_constant__ CacheParams p, const __grid_constant__ DecodePlan d) {
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long sh[10];
+  __shared__ long long sh[7];
+  __shared__ float fac[4][Core::kHeads], sum_sh[Core::kHeads];
   float* res = (float*)smem;
   constexpr int kUnit = Core::kUnit;
   ptx::grid_dep_launch();   // join_kernel may start (and wait)
-  long long dummy, total;
-  batch_units<kDecThr>(p, kUnit, 0, sh, dummy, total);
-  const int kcn = p.K * d.nchunk;
-  total *= kcn;
-  long long cur = (long long)blockIdx.x * total / d.C;
-  const long long start = cur, end = (long long)(blockIdx.x + 1) * total / d.C;
-  if (cur >= end) return;
-  int b;
-  long long before;
-  find_seq(p, kUnit, cur / kcn, sh, b, before);
-  const int hw = p.hd + 2;
+  const int kcn = p.K * d.nchunk, hw = p.hd + 2;
+  const Place pl = find_place(p, kUnit, d.C, kcn, sh);
+  long long cur = pl.start, before = pl.before;
+  const long long start = pl.start, end = pl.end;
+  int b = pl.b;
   while (cur < end) {
     Segment s;
     s.b = b;
@@ -594,9 +605,9 @@ __global__ void __launch_bounds__(kDecThr)
     const bool whole = s.u0 == 0 && s.u1 == U;
     const int slot = cur == start ? 0 : 1;
     float* part = d.part + ((long long)blockIdx.x * 2 + slot) * d.heads * d.hds;
-    for (int x = threadIdx.x; x < s.hc * p.hd; x += kDecThr) {
-      const int h = x / p.hd, c = x - h * p.hd;
-      float m[4], M = -INFINITY, L = 0.f, O = 0.f;
+    if ((int)threadIdx.x < s.hc) {
+      const int h = threadIdx.x;
+      float m[4], M = -INFINITY, L = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         m[w] = res[(w * Core::kHeads + h) * hw + p.hd];
@@ -605,24 +616,28 @@ __global__ void __launch_bounds__(kDecThr)
       const float mu = M == -INFINITY ? 0.f : M;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float f = exp2f(m[w] - mu);
-        L = fmaf(res[(w * Core::kHeads + h) * hw + p.hd + 1], f, L);
-        O = fmaf(res[(w * Core::kHeads + h) * hw + c], f, O);
+        fac[w][h] = exp2f(m[w] - mu);
+        L = fmaf(res[(w * Core::kHeads + h) * hw + p.hd + 1], fac[w][h], L);
       }
+      sum_sh[h] = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
       if (whole) {
-        seq_st((E*)p.out + ((long long)s.b * p.H + s.h0 + h) * p.hd + c, L == 0.f ? 0.f : O / L);
-        if (c == 0) {
-          const float z = lse2_of(M, L);
-          if (p.lse) p.lse[(long long)s.b * p.H + s.h0 + h] = z * kLn2;
-          d.lse2[(long long)s.b * p.H + s.h0 + h] = z;
-        }
+        const float z = lse2_of(M, L);
+        if (p.lse) p.lse[(long long)s.b * p.H + s.h0 + h] = z * kLn2;
+        d.lse2[(long long)s.b * p.H + s.h0 + h] = z;
       } else {
-        part[h * d.hds + c] = O;
-        if (c == 0) {
-          part[h * d.hds + p.hd] = M;
-          part[h * d.hds + p.hd + 1] = L;
-        }
+        part[h * d.hds + p.hd] = M;
+        part[h * d.hds + p.hd + 1] = L;
       }
+    }
+    __syncthreads();
+    E* out = (E*)p.out + ((long long)s.b * p.H + s.h0) * p.hd;
+    for (int x = threadIdx.x; x < s.hc * p.hd; x += kDecThr) {
+      const int h = x / p.hd, c = x - h * p.hd;
+      float O = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) O = fmaf(res[(w * Core::kHeads + h) * hw + c], fac[w][h], O);
+      if (whole) seq_st(out + x, O * sum_sh[h]);
+      else part[h * d.hds + c] = O;
     }
     // the new token's row: its position is the last of the last unit
     if (p.k_new && chunk == 0 && s.u1 == U) {
@@ -641,7 +656,7 @@ __global__ void __launch_bounds__(kDecThr)
 
 // Joins the pieces of the heads of (b, kh) that several blocks hold, writes
 // empty sequences, and adds the step's weights: blockIdx.y = piece of
-// kJoinSpan positions (0 also joins). Waits for decode_kernel, whose
+// kJoinSpan positions and of the outputs. Waits for decode_kernel, whose
 // programmatic dependent it is. Per chunk of query heads the pieces' slots are
 // listed once, a warp per head finds the common maximum and sum, and a thread
 // per channel adds the pieces in order.
@@ -653,7 +668,8 @@ __global__ void __launch_bounds__(kJoinThr)
   float* lse_sh = join_sh;                      // [G]
   float* inv_sh = lse_sh + p.G;                 // [heads]
   int* slots = (int*)(inv_sh + d.heads);        // [C]
-  float* fac = (float*)(slots + d.C);           // [heads][C]
+  float* fac = (float*)(slots + d.C);           // [heads][C]: maxima, then factors
+  float* sums = fac + d.heads * d.C;            // [heads][C]
   __shared__ long long sh[2 * kJoinThr / 32];
   const int b = blockIdx.x / p.K, kh = blockIdx.x - b * p.K;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -679,7 +695,6 @@ __global__ void __launch_bounds__(kJoinThr)
         for (int h = threadIdx.x; h < hc; h += kJoinThr) lse_sh[h0 + h] = d.lse2[bh0 + h0 + h];
       continue;
     }
-    if (blockIdx.y > 0 && !p.w_out) continue;
     const int ns = c1 - c0 + 1;
     __syncthreads();
     for (int k = threadIdx.x; k < ns; k += kJoinThr) {
@@ -689,23 +704,24 @@ __global__ void __launch_bounds__(kJoinThr)
       slots[k] = max(g0, s0) < min(g1, s1) ? 2 * c + (s0 >= g0 ? 0 : 1) : -1;
     }
     __syncthreads();
-    auto piece = [&](int k, int h) {
-      return d.part + ((long long)slots[k] * d.heads + h) * d.hds;
+    auto piece = [&](int k, int h) {   // (no slot: some slot's, not used)
+      return d.part + ((long long)max(slots[k], 0) * d.heads + h) * d.hds;
     };
     for (int h = warp; h < hc; h += kJoinThr / 32) {
       float M = -INFINITY, L = 0.f;
-      for (int k = lane; k < ns; k += 32)
-        if (slots[k] >= 0) M = fmaxf(M, piece(k, h)[p.hd]);
+      for (int k = lane; k < ns; k += 32) {
+        const float m = piece(k, h)[p.hd], l = piece(k, h)[p.hd + 1];
+        fac[h * d.C + k] = slots[k] >= 0 ? m : -INFINITY;
+        sums[h * d.C + k] = slots[k] >= 0 ? l : 0.f;
+        M = fmaxf(M, fac[h * d.C + k]);
+      }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       const float mu = M == -INFINITY ? 0.f : M;
       for (int k = lane; k < ns; k += 32) {
-        float f = 0.f;
-        if (slots[k] >= 0) {
-          f = exp2f(piece(k, h)[p.hd] - mu);
-          L = fmaf(piece(k, h)[p.hd + 1], f, L);
-        }
+        const float f = exp2f(fac[h * d.C + k] - mu);
         fac[h * d.C + k] = f;
+        L = fmaf(sums[h * d.C + k], f, L);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
@@ -717,12 +733,14 @@ __global__ void __launch_bounds__(kJoinThr)
       }
     }
     __syncthreads();
-    for (int x = threadIdx.x; x < hc * p.hd && blockIdx.y == 0; x += kJoinThr) {
+    for (int x = blockIdx.y * kJoinThr + threadIdx.x; x < hc * p.hd; x += kJoinThr * gridDim.y) {
       const int h = x / p.hd, c = x - h * p.hd;
       float O = 0.f;
-#pragma unroll 8
-      for (int k = 0; k < ns; ++k)
-        if (slots[k] >= 0) O = fmaf(piece(k, h)[c], fac[h * d.C + k], O);
+#pragma unroll 16
+      for (int k = 0; k < ns; ++k) {
+        const float o = piece(k, h)[c];
+        O = fmaf(slots[k] >= 0 ? o : 0.f, fac[h * d.C + k], O);
+      }
       seq_st((E*)p.out + (bh0 + h0 + h) * p.hd + c, O * inv_sh[h]);
     }
   }
@@ -759,47 +777,40 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 constexpr int kSelThr = 1024, kSelRegs = 32;   // positions held in registers: 32 x 1024
 
 struct SelectShared {
-  uint32_t hist[32 * 256];   // per warp; then counts in position order
+  uint32_t hist[4 * 2048];   // four copies; then counts in position order
   uint32_t bin, need, warp_sum[32];
 };
 
-// One digit of the threshold from the block's histograms: the bin that holds the
-// need-th largest key and how many of it are needed.
+// One digit of the threshold from the block's histograms (2048 bins, two a
+// thread, from the top): the bin that holds the need-th largest key and how many
+// of it are needed.
 __device__ __forceinline__ void pick_bin(SelectShared& sh, uint32_t need) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, top = 2047 - 2 * threadIdx.x;
   __syncthreads();
-  if (threadIdx.x < 256) {
-    uint32_t s = 0;
+  uint32_t c0 = 0, c1 = 0;   // bins top, top - 1
 #pragma unroll
-    for (int v = 0; v < 32; ++v) s += sh.hist[v * 256 + threadIdx.x];
-    sh.hist[threadIdx.x] = s;
+  for (int v = 0; v < 4; ++v) {
+    const uint2 h = *reinterpret_cast<const uint2*>(&sh.hist[v * 2048 + top - 1]);
+    c0 += h.y;
+    c1 += h.x;
   }
+  const uint32_t sum = c0 + c1;
+  uint32_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  if (lane == 31) sh.warp_sum[warp] = inc;
   __syncthreads();
-  if (threadIdx.x < 32) {   // bins from the top, eight a lane
-    const int lane = threadIdx.x;
-    uint32_t c[8], sum = 0;
+  uint32_t t = lane < warp ? sh.warp_sum[lane] : 0u;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      c[e] = sh.hist[255 - (lane * 8 + e)];
-      sum += c[e];
-    }
-    uint32_t inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t t = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += t;
-    }
-    uint32_t before = inc - sum;
-    if (before < need && need <= inc) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (before < need && need <= before + c[e]) {
-          sh.bin = 255 - (lane * 8 + e);
-          sh.need = need - before;
-          break;
-        }
-        before += c[e];
-      }
-    }
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  const uint32_t before = t + inc - sum;
+  if (before < need && need <= before + sum) {
+    const bool first = need <= before + c0;
+    sh.bin = first ? top : top - 1;
+    sh.need = first ? need - before : need - before - c0;
   }
   __syncthreads();
 }
@@ -807,7 +818,8 @@ __device__ __forceinline__ void pick_bin(SelectShared& sh, uint32_t need) {
 // Which positions of (b, kv head) stay: one block each. The always-kept positions
 // have the largest key, so what stays is the `budget` largest keys of the
 // sequence, ties at the threshold in order of position. The threshold is found
-// digit by digit (four passes over 8 bits, a histogram per warp). A kept
+// digit by digit (11, 11 and 10 bits; wide digits, since weights share few
+// exponents and shared-memory atomics on one bin queue up). A kept
 // position's place in the output is the number of larger keys before it plus
 // the ties before it that stay. With R > 0 a thread holds its R positions (1024
 // apart) in registers and one scan over the counts of every warp and round
@@ -818,7 +830,7 @@ __device__ __forceinline__ void pick_bin(SelectShared& sh, uint32_t need) {
 template <int R>
 __global__ void __launch_bounds__(kSelThr)
     evict_select_kernel(const __grid_constant__ CacheParams p, int* kept) {
-  __shared__ SelectShared sh;
+  __shared__ __align__(16) SelectShared sh;
   ptx::grid_dep_launch();
   const int b = blockIdx.x / p.K, kh = blockIdx.x - b * p.K;
   const int n = cache_len(p, b), keep = min(n, p.budget);
@@ -831,11 +843,20 @@ __global__ void __launch_bounds__(kSelThr)
   auto key_of = [&](int x) {
     return x >= n ? 0u : (x < lo || x >= hi ? 0xffffffffu : weight_key(w[x]));
   };
-  uint32_t keys[R > 0 ? R : 1];
+  uint32_t keys[R > 0 ? R : 1];   // weights as they come, then keys
   const int rounds = R > 0 ? min(R, (n + kSelThr - 1) / kSelThr) : (n + kSelThr - 1) / kSelThr;
   if constexpr (R > 0) {
+    // all loads first
 #pragma unroll
-    for (int r = 0; r < R; ++r) keys[r] = r < rounds ? key_of(r * kSelThr + threadIdx.x) : 0u;
+    for (int r = 0; r < R; ++r)
+      keys[r] = r < rounds
+                    ? __float_as_uint(w[min(r * kSelThr + (int)threadIdx.x, n - 1)]) : 0u;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int x = r * kSelThr + threadIdx.x;
+      const uint32_t k = weight_key(__uint_as_float(keys[r]));
+      keys[r] = x >= n ? 0u : (x < lo || x >= hi ? 0xffffffffu : k);
+    }
   }
   for (int x = keep + threadIdx.x; x < p.budget; x += kSelThr) out[x] = -1;
   for (long long x = keep + threadIdx.x; x < p.max_len; x += kSelThr) w_out[x] = 0.f;
@@ -848,23 +869,29 @@ __global__ void __launch_bounds__(kSelThr)
   }
   uint32_t prefix = 0, need = (uint32_t)p.budget;
 #pragma unroll 1
-  for (int pass = 0; pass < 4; ++pass) {
-    const int bits = 24 - 8 * pass;
-#pragma unroll
-    for (int x = 0; x < 8; ++x) sh.hist[x * kSelThr + threadIdx.x] = 0;
+  for (int pass = 0; pass < 3; ++pass) {
+    const int bits = pass == 0 ? 21 : (pass == 1 ? 10 : 0);       // below the digit
+    const int above = pass == 0 ? 0 : (pass == 1 ? 21 : 10);      // 0: every key counts
+    const uint32_t digit = pass == 2 ? 1023u : 2047u;
+    uint4* z = reinterpret_cast<uint4*>(sh.hist);
+    z[threadIdx.x] = z[kSelThr + threadIdx.x] = make_uint4(0, 0, 0, 0);
     __syncthreads();
+    uint32_t* mine = sh.hist + (warp & 3) * 2048;
     auto count = [&](uint32_t k) {
-      if (k != 0 && (pass == 0 || (k >> (bits + 8)) == prefix))
-        atomicAdd(&sh.hist[warp * 256 + ((k >> bits) & 255)], 1u);
+      if (k != 0 && (pass == 0 || (k >> above) == prefix))
+        atomicAdd(&mine[(k >> bits) & digit], 1u);
     };
     if constexpr (R > 0) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) count(keys[r]);
+      for (int r = 0; r < R; ++r) {
+        if (r >= rounds) break;
+        count(keys[r]);
+      }
     } else {
       for (int r = 0; r < rounds; ++r) count(key_of(r * kSelThr + threadIdx.x));
     }
     pick_bin(sh, need);
-    prefix = (prefix << 8) | sh.bin;
+    prefix = pass == 0 ? sh.bin : (prefix << (pass == 1 ? 11 : 10)) | sh.bin;
     need = sh.need;
     __syncthreads();
   }
@@ -882,7 +909,7 @@ __global__ void __launch_bounds__(kSelThr)
   if constexpr (R > 0) {
     // larger keys and ties (high half) of every round and warp, in position order
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < R; ++r) {   // (all R: the scan reads every entry)
       const uint32_t gt = __ballot_sync(0xffffffffu, keys[r] > thr);
       const uint32_t eq = __ballot_sync(0xffffffffu, keys[r] == thr);
       if (lane == 0) sh.hist[r * 32 + warp] = __popc(gt) | (__popc(eq) << 16);
@@ -1029,9 +1056,11 @@ cudaError_t decode_go(const CacheParams& p, const DecodePlan& d, cudaStream_t st
   note_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const unsigned pieces = p.w_out ? (unsigned)((p.max_len + kJoinSpan - 1) / kJoinSpan) : 1;
+  const long long outs = ((long long)d.heads * p.hd + kJoinThr - 1) / kJoinThr;
+  const long long spans = p.w_out ? (p.max_len + kJoinSpan - 1) / kJoinSpan : 1;
+  const unsigned pieces = (unsigned)(outs > spans ? outs : spans);
   if (pieces > 65535) return cudaErrorInvalidConfiguration;
-  const size_t smem = (size_t)(p.G + d.heads + d.C + d.heads * d.C) * 4;
+  const size_t smem = (size_t)(p.G + d.heads + d.C + 2 * d.heads * d.C) * 4;
   return launch_dependent(join_kernel<E>, dim3(p.B * p.K, pieces), kJoinThr, smem, st, p, d);
 }
 
