@@ -776,6 +776,12 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 constexpr int kSelThr = 1024, kSelRegs = 32;   // positions held in registers: 32 x 1024
 
+__device__ __forceinline__ uint32_t load_once(const float* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 struct SelectShared {
   uint32_t hist[4 * 2048];   // four copies; then counts in position order
   uint32_t bin, need, warp_sum[32];
@@ -846,11 +852,14 @@ __global__ void __launch_bounds__(kSelThr)
   uint32_t keys[R > 0 ? R : 1];   // weights as they come, then keys
   const int rounds = R > 0 ? min(R, (n + kSelThr - 1) / kSelThr) : (n + kSelThr - 1) / kSelThr;
   if constexpr (R > 0) {
-    // all loads first
+    // all loads first, in flight together (left to itself the compiler waits for each)
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      keys[r] = r < rounds
-                    ? __float_as_uint(w[min(r * kSelThr + (int)threadIdx.x, n - 1)]) : 0u;
+    for (int r = 0; r < R; ++r) {
+      keys[r] = 0u;
+      if (r < rounds)
+        keys[r] = load_once(w + min(r * kSelThr + (int)threadIdx.x, max(n - 1, 0)));
+    }
+    asm volatile("" ::: "memory");
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int x = r * kSelThr + threadIdx.x;
@@ -896,14 +905,14 @@ __global__ void __launch_bounds__(kSelThr)
     __syncthreads();
   }
   const uint32_t thr = prefix, lt = (1u << lane) - 1u;
-  auto emit = [&](int x, uint32_t k, uint32_t gt_before, uint32_t eq_before) {
+  auto emit = [&](int x, uint32_t k, uint32_t gt_before, uint32_t eq_before, float weight) {
     const uint32_t gt = __ballot_sync(0xffffffffu, k > thr);
     const uint32_t eq = __ballot_sync(0xffffffffu, k == thr);
     const uint32_t tie = eq_before + __popc(eq & lt);
     if (k > thr || (k == thr && tie < need)) {
       const uint32_t at = gt_before + __popc(gt & lt) + min(tie, need);
       out[at] = x;
-      w_out[at] = w[x];
+      w_out[at] = weight;
     }
   };
   if constexpr (R > 0) {
@@ -928,11 +937,23 @@ __global__ void __launch_bounds__(kSelThr)
     for (int v = 0; v < warp; ++v) base += sh.warp_sum[v];
     if ((int)threadIdx.x < R * 32) sh.hist[threadIdx.x] = base + inc - c;
     __syncthreads();
+    // (the weights once more, eight in flight: a key does not give back NaN and -0)
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (r >= rounds) break;
-      const uint32_t before = sh.hist[r * 32 + warp];
-      emit(r * kSelThr + threadIdx.x, keys[r], before & 0xffffu, before >> 16);
+    for (int r0 = 0; r0 < R; r0 += 8) {
+      if (r0 >= rounds) break;
+      uint32_t raw[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (r0 + e < R)
+          raw[e] = load_once(w + min((r0 + e) * kSelThr + (int)threadIdx.x, n - 1));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int r = r0 + e;
+        if (r >= R) break;
+        const uint32_t before = sh.hist[r * 32 + warp];
+        emit(r * kSelThr + threadIdx.x, keys[r], before & 0xffffu, before >> 16,
+             __uint_as_float(raw[e]));
+      }
     }
   } else {
     const int per = ((n + 31) / 32 + 31) / 32 * 32;   // positions of a warp
@@ -960,7 +981,7 @@ __global__ void __launch_bounds__(kSelThr)
     }
     for (int x = x0; x < x1; x += 32) {
       const uint32_t k = x + lane < x1 ? key_of(x + lane) : 0u;
-      emit(x + lane, k, gt, eq);
+      emit(x + lane, k, gt, eq, w[min(x + lane, n - 1)]);
       gt += __popc(__ballot_sync(0xffffffffu, k > thr));
       eq += __popc(__ballot_sync(0xffffffffu, k == thr));
     }
