@@ -68,30 +68,31 @@ struct BwdItem {
     else return passes == 2;
   }
 };
-// Walks an item's steps in order: first streamed token and query head of each.
+// Walks an item's steps in order: first streamed token and query head of each (with
+// what it needs of the item in registers).
 template <bool KEYS>
 struct StepWalk {
   int row, head, x;
-  __device__ __forceinline__ void start(const BwdItem<KEYS>& it) {
-    x = 0;
-    if constexpr (KEYS) {
-      row = it.d.i0;
-      head = it.d.h0;
-    } else {
-      row = it.kt.tile(0) * kStep;
-      head = it.h;
-    }
+  int i0, i1, s, lo;
+  __device__ __forceinline__ explicit StepWalk(const BwdItem<KEYS>& it)
+      : i0(KEYS ? it.d.i0 : 0), i1(KEYS ? it.d.i1 : 0), s(it.kt.s), lo(it.kt.lo * kStep) {
+    head = KEYS ? it.d.h0 : it.h;
+    start();
   }
-  __device__ __forceinline__ void next(const BwdItem<KEYS>& it) {
+  __device__ __forceinline__ void start() {
+    x = 0;
+    row = KEYS ? i0 : (s > 0 ? 0 : lo);
+  }
+  __device__ __forceinline__ void next() {
     ++x;
     row += kStep;
     if constexpr (KEYS) {
-      if (row >= it.d.i1) {
-        row = it.d.i0;
+      if (row >= i1) {
+        row = i0;
         ++head;
       }
     } else {
-      if (x == it.kt.s) row = it.kt.lo * kStep;
+      if (x == s) row = lo;
     }
   }
 };
@@ -272,8 +273,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
           ++k;
           const int kh = it.h / p.G;
           for (int ps = 0; ps < it.passes && ok; ++ps) {
-            StepWalk<KEYS> w;
-            for (w.start(it); w.x < it.steps; w.next(it), rb.next(), ++e) {
+            for (StepWalk<KEYS> w(it); w.x < it.steps; w.next(), rb.next(), ++e) {
               if (!seq_wait(&b_empty[rb.s], rb.parity ^ 1, abort, p.status)) {
                 ok = false;
                 break;
@@ -368,8 +368,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
         const bool grads = ps == it.passes - 1;
         if (grads) ok = warp_wait(&acc_empty[acc.s], acc.parity ^ 1, abort, p.status);
         const uint32_t to = uniform(tmem + TM::kAccCol + acc.s * TM::kAccCols);
-        StepWalk<KEYS> w;
-        for (w.start(it); ok && w.x < it.steps; w.next(it), rb.next(), buf.next()) {
+        for (StepWalk<KEYS> w(it); ok && w.x < it.steps; w.next(), rb.next(), buf.next()) {
           ok = warp_wait(&b_full[rb.s], rb.parity, abort, p.status);
           if (!ok) break;
           if (grads && w.row + kStep > it.n) {
@@ -452,12 +451,12 @@ __global__ void __launch_bounds__(kBThreads, 1)
         }
       }
       float dsum = 0.f;
-      StepWalk<KEYS> w;
-      if (it.steps) w.start(it);
-      const int total = it.steps * it.passes;
-      for (int x = 0; x < total; ++x, ++turn, w.next(it), rb.next(), rbuf.next()) {
-        if (!KEYS && x == it.steps) {
-          w.start(it);
+      StepWalk<KEYS> w(it);
+      const int steps = it.steps, total = steps * it.passes, r0 = it.r0;
+      const int i1 = KEYS ? it.d.i1 : 0;
+      for (int x = 0; x < total; ++x, ++turn, w.next(), rb.next(), rbuf.next()) {
+        if (!KEYS && x == steps) {
+          w.start();
           // D of the row: the two warpgroups' parts, in order
           xch[wg * kRows + row] = dsum;
           named_sync(1, kSoft * 32);
@@ -480,23 +479,23 @@ __global__ void __launch_bounds__(kBThreads, 1)
         bool plain;
         if constexpr (KEYS) {
           lo = r - c0;
-          hi = it.d.i1 - 1;
+          hi = i1 - 1;
           if (r >= p.sinks && p.window <= 0x7fffffff - r) hi = min(hi, r + p.window - 1);
           hi -= c0;
-          plain = c0 >= it.r0 + kRows - 1 && c0 + kStep <= it.d.i1 &&
-                  (c0 + kStep - 1 - it.r0 < p.window || it.r0 + kRows <= p.sinks);
+          plain = c0 >= r0 + kRows - 1 && c0 + kStep <= i1 &&
+                  (c0 + kStep - 1 - r0 < p.window || r0 + kRows <= p.sinks);
         } else {
           hi = r - c0;
           lo = hi - p.window + 1;
           sk = p.sinks - c0;
-          plain = c0 + kStep - 1 <= it.r0 &&
-                  (it.r0 + kRows - 1 - c0 < p.window || c0 + kStep <= p.sinks);
+          plain = c0 + kStep - 1 <= r0 &&
+                  (r0 + kRows - 1 - c0 < p.window || c0 + kStep <= p.sinks);
         }
-        const bool sums = !KEYS && it.passes == 2 && x < it.steps;   // the pass for D
+        const bool sums = !KEYS && x < total - steps;   // the pass for D
         const float4* lv = reinterpret_cast<const float4*>(lds + rb.s * 2 * kStep);
         const float4* dv = lv + kStep / 4;
         const float sub = sums ? 0.f : nd;
-        const bool few = it.few(p, w.row);
+        const bool few = KEYS ? it.few(p, c0) : total > steps;
         tmem_wait_ld();
 #pragma unroll
         for (int h = 0; h < kStep; h += 32) {
