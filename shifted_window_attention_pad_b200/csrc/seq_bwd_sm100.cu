@@ -22,9 +22,9 @@
 // pay two more products per step for an error already below the outputs' own
 // rounding.
 //
-// Warps: 0-3 and 4-7 a softmax warpgroup each, taking the steps in turn (thread =
-// row); 8 the TMA producer; 9 issues S and dP and owns TMEM; 10 issues the
-// gradient products. Bound: the tensor pipe at head_dim 128 (per 128 x 64 step S
+// Warps: a softmax warpgroup per TMEM buffer, taking the steps in turn (thread =
+// row); then the TMA producer, a warp that issues S and dP and owns TMEM, and one
+// that issues the gradient products. Bound: the tensor pipe at head_dim 128 (per 128 x 64 step S
 // and dP with N = 64, which read both operands from shared memory at 1.5 times
 // the cost of N = 128, and one or two gradient products), the exp unit and the
 // softmax warps' issue slots at 64.
@@ -36,9 +36,6 @@ namespace {
 using namespace ptx;
 
 constexpr int kStep = 64;         // keys (queries) of a step
-constexpr int kSoft = 8;          // softmax warps
-constexpr int kBProducer = 8, kBMma = 9, kBMma2 = 10;
-constexpr int kBThreads = 11 * 32;
 // TMEM: NB buffers of S | dP, then ND accumulators of HD columns (dQ) or 2 HD
 // (dV, dK). Three buffers let a step's products start while the two softmax
 // pairs work on those before; head_dim 128 leaves the key side two.
@@ -46,6 +43,9 @@ template <int HD, bool KEYS>
 struct BwdTmem {
   static constexpr int NB = KEYS && HD > 64 ? 2 : 3;
   static constexpr int ND = KEYS || HD > 64 ? 1 : 2;
+  static constexpr int NW = NB;                 // softmax warpgroups, one per buffer
+  static constexpr int kSoft = 4 * NW;          // their warps; then producer and MMA warps
+  static constexpr int kThreads = (kSoft + 3) * 32;
   static constexpr uint32_t kAccCol = NB * 2 * kStep;
   static constexpr uint32_t kAccCols = KEYS ? 2 * HD : HD;
   static_assert(kAccCol + ND * kAccCols <= 512, "TMEM columns");
@@ -134,7 +134,7 @@ struct BwdCfg {
   static constexpr uint32_t kRing = kABufs * 2 * kTile;
   static constexpr uint32_t kLd = kRing + kStages * 2 * kSub;
   static constexpr uint32_t kXch = kLd + (KEYS ? kStages * kStep : kABufs * kRows) * 8;
-  static constexpr uint32_t kBars = kXch + 2 * kRows * 4;
+  static constexpr uint32_t kBars = kXch + 3 * kRows * 4;
   static constexpr uint32_t kFeedAt = kBars + 8 * 40;
   static constexpr uint32_t kTotal = kFeedAt + sizeof(Feed<BwdItem<KEYS>>) + 16;
   static constexpr uint32_t kSmem = kTotal + 1024;
@@ -176,14 +176,15 @@ __device__ __forceinline__ bool store_grad(uint32_t col, float mul, bool keep, v
 }
 
 template <int HD, bool KEYS>
-__global__ void __launch_bounds__(kBThreads, 1)
+__global__ void __launch_bounds__(BwdTmem<HD, KEYS>::kThreads, 1)
     seq_bwd_kernel(const __grid_constant__ SeqParams p,
                    const __grid_constant__ BwdMaps maps) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   using C = BwdCfg<HD, KEYS>;
   using TM = BwdTmem<HD, KEYS>;
-  constexpr int NA = C::kABufs, NS = C::kStages, NB = TM::NB, ND = TM::ND;
+  constexpr int NA = C::kABufs, NS = C::kStages, NB = TM::NB, ND = TM::ND, NW = TM::NW;
+  constexpr int kSoft = TM::kSoft, kBProducer = kSoft, kBMma = kSoft + 1, kBMma2 = kSoft + 2;
   constexpr uint32_t TB = C::kTile, SB = C::kSub;
   uint8_t* abuf = smem;
   uint8_t* ring = smem + C::kRing;
@@ -386,13 +387,14 @@ __global__ void __launch_bounds__(kBThreads, 1)
           const bool few = it.few(p, w.row);
           if (elect_one()) {
             if (grads) {
-              // A from TMEM: 16 elements of K are 8 columns; low parts 32 behind high
+              // A from TMEM: 16 elements of K are 8 columns; split, the 32 columns of
+              // each half of the step hold its high parts, then its low ones
 #pragma unroll
               for (int part = 0; part < 2; ++part) {
                 if (part && !few) break;
 #pragma unroll
                 for (int kk = 0; kk < kStep / 16; ++kk) {
-                  const uint32_t a = d + 8 * kk + 32 * part;
+                  const uint32_t a = d + (few ? 32 * (kk >> 1) + 8 * (kk & 1) + 16 * part : 8 * kk);
                   const uint32_t add = on | (part > 0) | (kk > 0);
                   if constexpr (KEYS) {
                     umma_ts(to, a, b1 + mnmajor_step(kk), idesc, add);
@@ -419,10 +421,9 @@ __global__ void __launch_bounds__(kBThreads, 1)
       mbar_drain(&drain[1], 0, kTestLimitNs * 100);
     }
   } else if (warp < kSoft) {
-    // Warpgroup wg takes every second step; thread = row (query or key) = TMEM lane.
+    // Warpgroup wg takes the steps of buffer wg; thread = row (query or key) = TMEM lane.
     // Waits name a round of a barrier by its parity; none can be mistaken here:
-    // products are issued in order, and S of step e + NB not before the warpgroup of
-    // step e has written P.
+    // S of a buffer's next step is not issued before P of this one is written.
     const int wg = warp >> 2, row = threadIdx.x & (kWg - 1);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
@@ -430,10 +431,9 @@ __global__ void __launch_bounds__(kBThreads, 1)
     Ring<NS> rb;
     Ring<NB> rbuf;
     Ring<ND> racc;
-    uint32_t turn = 0;   // steps so far
     for (;;) {
       const Item* item = rd.next(abort, p.status);
-      // both warpgroups go on together
+      // the warpgroups go on together
       if (named_sync_or(1, kSoft * 32, !item || *abort)) break;
       const Item& it = *item;
       const int r = it.r0 + row;
@@ -454,26 +454,23 @@ __global__ void __launch_bounds__(kBThreads, 1)
       StepWalk<KEYS> w(it);
       const int steps = it.steps, total = steps * it.passes, r0 = it.r0;
       const int i1 = KEYS ? it.d.i1 : 0;
-      for (int x = 0; x < total; ++x, ++turn, w.next(), rb.next(), rbuf.next()) {
+      for (int x = 0; x < total; ++x, w.next(), rb.next(), rbuf.next()) {
         if (!KEYS && x == steps) {
           w.start();
-          // D of the row: the two warpgroups' parts, in order
+          // D of the row: the warpgroups' parts, in order
           xch[wg * kRows + row] = dsum;
           named_sync(1, kSoft * 32);
-          nd = -(xch[row] + xch[kRows + row]);
+          nd = xch[row];
+#pragma unroll
+          for (int y = 1; y < NW; ++y) nd += xch[y * kRows + row];
+          nd = -nd;
           if (wg == 0 && real) p.nd[((long long)it.b * p.H + it.h) * p.ld_stride + r] = nd;
         }
-        if ((int)(turn & 1) != wg) continue;
+        if (rbuf.s != wg) continue;
         const uint32_t s_col = tmem + lane_base + rbuf.s * 2 * kStep;
         const int c0 = w.row;   // first token of the step's columns
         seq_wait(&s_full[rbuf.s], rbuf.parity, abort, p.status);
         tc_fence_after();
-        float v[kStep], g[kStep];
-        __syncwarp();
-        tmem_ld32(s_col, v);
-        tmem_ld32(s_col + 32, v + 32);
-        tmem_ld32(s_col + kStep, g);
-        tmem_ld32(s_col + kStep + 32, g + 32);
         // visible columns of the row: lo .. hi, and below sk
         int lo, hi, sk = 0;
         bool plain;
@@ -496,16 +493,23 @@ __global__ void __launch_bounds__(kBThreads, 1)
         const float4* dv = lv + kStep / 4;
         const float sub = sums ? 0.f : nd;
         const bool few = KEYS ? it.few(p, c0) : total > steps;
-        tmem_wait_ld();
+        // a half of the step's columns at a time (two halves in registers at once, with
+        // two warpgroups of twice the registers: 150 us against the figure above)
 #pragma unroll
         for (int h = 0; h < kStep; h += 32) {
+          float v[32], g[32];
+          __syncwarp();
+          tmem_ld32(s_col + h, v);
+          tmem_ld32(s_col + kStep + h, g);
+          tmem_wait_ld_regs(v);
+          reg_fence32(g);
           // P = 2^(c S - L) and dS = P (dP - D)
 #pragma unroll
-          for (int j = h; j < h + 32; j += 4) {
+          for (int j = 0; j < 32; j += 4) {
             float4 l4 = make_float4(nl, nl, nl, nl), d4 = make_float4(sub, sub, sub, sub);
             if constexpr (KEYS) {   // of four queries
-              l4 = lv[j / 4];
-              d4 = dv[j / 4];
+              l4 = lv[(h + j) / 4];
+              d4 = dv[(h + j) / 4];
             }
             const float2 a = __ffma2_rn(make_float2(v[j], v[j + 1]), c2, make_float2(l4.x, l4.y));
             const float2 b = __ffma2_rn(make_float2(v[j + 2], v[j + 3]), c2, make_float2(l4.z, l4.w));
@@ -521,7 +525,7 @@ __global__ void __launch_bounds__(kBThreads, 1)
             g[j + 3] = gb.y;
           }
 #pragma unroll
-          for (int j = h; j < h + 32; j += 2) {
+          for (int j = 0; j < 32; j += 2) {
             const float2 e = __fmul2_rn(make_float2(g[j], g[j + 1]), make_float2(v[j], v[j + 1]));
             g[j] = e.x;
             g[j + 1] = e.y;
@@ -531,33 +535,35 @@ __global__ void __launch_bounds__(kBThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (!(see & (1u << j))) {
-                if constexpr (KEYS) v[h + j] = 0.f;
-                g[h + j] = 0.f;
+                if constexpr (KEYS) v[j] = 0.f;
+                g[j] = 0.f;
               }
           }
           if (sums) {
             float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-            for (int j = h; j < h + 32; j += 2) {
+            for (int j = 0; j < 32; j += 2) {
               a0 += g[j];
               a1 += g[j + 1];
             }
             dsum += a0 + a1;
           } else {
-            const uint32_t s_to = s_col + h / 2, d_to = s_to + (KEYS ? kStep : 0);
+            // over columns that this half's loads have emptied
             if (few) {
-              if constexpr (KEYS) split_to_columns(s_to, s_to + 32, v + h);
-              split_to_columns(d_to, d_to + 32, g + h);
+              const uint32_t to = s_col + h;
+              if constexpr (KEYS) split_to_columns(to, to + 16, v);
+              split_to_columns(to + (KEYS ? kStep : 0), to + (KEYS ? kStep : 0) + 16, g);
             } else {
+              const uint32_t to = s_col + h / 2;
               uint32_t pk[16];
               if constexpr (KEYS) {
-                round_pairs(v + h, pk);
+                round_pairs(v, pk);
                 __syncwarp();
-                tmem_st16u(s_to, pk);
+                tmem_st16u(to, pk);
               }
-              round_pairs(g + h, pk);
+              round_pairs(g, pk);
               __syncwarp();
-              tmem_st16u(d_to, pk);
+              tmem_st16u(to + (KEYS ? kStep : 0), pk);
             }
           }
         }
@@ -565,36 +571,39 @@ __global__ void __launch_bounds__(kBThreads, 1)
         tc_fence_before();
         mbar_arrive(&p_full[rbuf.s]);
       }
-      // epilogue: a warpgroup stores half of the accumulator columns (dV or dK)
-      constexpr int NC = TM::kAccCols / 2;
-      if (it.steps) {
-        seq_wait(&acc_full[racc.s], racc.parity, abort, p.status);
-        tc_fence_after();
+      // epilogue: two warpgroups store half of the accumulator columns each (dV, dK)
+      bool bad = false;
+      if (wg < 2) {
+        constexpr int NC = TM::kAccCols / 2;
+        if (it.steps) {
+          seq_wait(&acc_full[racc.s], racc.parity, abort, p.status);
+          tc_fence_after();
+        }
+        const uint32_t acc = tmem + lane_base + TM::kAccCol + racc.s * TM::kAccCols + wg * NC;
+        void* dst;
+        bool f32 = false;
+        float mul = p.scale;
+        if constexpr (KEYS) {
+          f32 = it.d.partial;
+          if (f32) dst = (wg == 0 ? it.d.pv : it.d.pk) + row * it.d.row_stride;
+          else
+            dst = (__nv_bfloat16*)(wg == 0 ? p.dv : p.dk) +
+                  ((long long)it.b * p.S + r) * p.ks + (long long)it.h * p.hd;
+          if (wg == 0) mul = 1.f;
+        } else {
+          dst = (__nv_bfloat16*)p.dq + ((long long)it.b * p.S + r) * p.qs +
+                (long long)it.h * p.hd + wg * NC;
+        }
+        if (!stored || *abort) dst = nullptr;
+        // an item without steps has no products: its rows are zeros whatever TMEM holds
+        bad = store_grad<NC>(acc, mul, real && it.steps, dst, f32,
+                                         p.hd - (KEYS ? 0 : wg * NC)) && real && it.steps;
+        if (it.steps) {
+          tc_fence_before();
+          mbar_arrive(&acc_empty[racc.s]);
+        }
       }
-      const uint32_t acc = tmem + lane_base + TM::kAccCol + racc.s * TM::kAccCols + wg * NC;
-      void* dst;
-      bool f32 = false;
-      float mul = p.scale;
-      if constexpr (KEYS) {
-        f32 = it.d.partial;
-        if (f32) dst = (wg == 0 ? it.d.pv : it.d.pk) + row * it.d.row_stride;
-        else
-          dst = (__nv_bfloat16*)(wg == 0 ? p.dv : p.dk) +
-                ((long long)it.b * p.S + r) * p.ks + (long long)it.h * p.hd;
-        if (wg == 0) mul = 1.f;
-      } else {
-        dst = (__nv_bfloat16*)p.dq + ((long long)it.b * p.S + r) * p.qs +
-              (long long)it.h * p.hd + wg * NC;
-      }
-      if (!stored || *abort) dst = nullptr;
-      // an item without steps has no products: its rows are zeros whatever TMEM holds
-      const bool bad = store_grad<NC>(acc, mul, real && it.steps, dst, f32,
-                                       p.hd - (KEYS ? 0 : wg * NC)) && real && it.steps;
-      if (it.steps) {
-        tc_fence_before();
-        mbar_arrive(&acc_empty[racc.s]);
-        racc.next();
-      }
+      if (it.steps) racc.next();
       if (named_sync_or(1, kSoft * 32, bad && !*abort)) {
         int* flags = (int*)xch;
         if (wg == 0) flags[row] = 0;
@@ -627,7 +636,7 @@ cudaError_t bwd_launch(const SeqParams& p, const BwdMaps& maps, cudaStream_t st)
   const long long items =
       KEYS ? p.plan.items : (long long)p.B * p.H * ((p.S + kRows - 1) / kRows);
   if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  seq_bwd_kernel<HD, KEYS><<<(unsigned)items, kBThreads, C::kSmem, st>>>(p, maps);
+  seq_bwd_kernel<HD, KEYS><<<(unsigned)items, BwdTmem<HD, KEYS>::kThreads, C::kSmem, st>>>(p, maps);
   note_launch();
   return cudaGetLastError();
 }
