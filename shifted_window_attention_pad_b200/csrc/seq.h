@@ -65,7 +65,7 @@ struct SeqParams {
 DkvPlan make_dkv_plan(int B, int S, int K, int G, int hd, int window, int sinks, int T);
 
 // Portable kernels; T of their key tiles.
-int seq_generic_tile(int hd);
+int seq_generic_tile(int B, int S, int H, int hd);
 cudaError_t seq_generic_forward(const SeqParams& p, int dtype, cudaStream_t st);
 cudaError_t seq_generic_backward(const SeqParams& p, int dtype, cudaStream_t st);
 // (-lse log2 e, -D) of every row, and the sum of the partials: both families.

@@ -69,7 +69,7 @@ SeqParams seq_params(const swin_seqattn_desc* d) {
   p.test_timeout = (d->flags & SWIN_FLAG_TEST_TIMEOUT) ? 1 : 0;
   p.ld_stride = ((long long)d->S + 127) / 128 * 128;
   p.plan = make_dkv_plan(p.B, p.S, p.K, p.G, p.hd, p.window, p.sinks,
-                         seq_fast(d) ? 128 : seq_generic_tile(p.hd));
+                         seq_fast(d) ? 128 : seq_generic_tile(p.B, p.S, p.H, p.hd));
   return p;
 }
 

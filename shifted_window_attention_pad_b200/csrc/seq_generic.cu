@@ -20,8 +20,6 @@ namespace {
 
 constexpr int kThr = 256;
 
-template <int HD>
-constexpr int tile_of() { return HD > 128 ? 32 : 64; }
 
 // rows row0 .. row0 + T - 1 (those below `rows` real, others zero) of hd channels
 template <typename E, int HD, int T>
@@ -145,9 +143,9 @@ __device__ __forceinline__ void flag_rows(const float (&acc)[R][NC], int* flags,
   }
 }
 
-template <typename E, int HD>
+template <typename E, int HD, int T>
 __global__ void __launch_bounds__(kThr) gen_fwd_kernel(const __grid_constant__ SeqParams p) {
-  constexpr int T = tile_of<HD>(), R = T / 16, NC = HD / 16;
+  constexpr int R = T / 16, NC = HD / 16;
   using C = Cols<HD>;
   extern __shared__ float sm[];
   float* qs = sm;
@@ -236,9 +234,9 @@ __global__ void __launch_bounds__(kThr) gen_fwd_kernel(const __grid_constant__ S
     if (flags[row] && i0 + row < n) fix_out_row<E>(p, b, h, i0 + row);
 }
 
-template <typename E, int HD>
+template <typename E, int HD, int T>
 __global__ void __launch_bounds__(kThr) gen_dq_kernel(const __grid_constant__ SeqParams p) {
-  constexpr int T = tile_of<HD>(), R = T / 16, NC = HD / 16;
+  constexpr int R = T / 16, NC = HD / 16;
   using C = Cols<HD>;
   extern __shared__ float sm[];
   float* qs = sm;
@@ -310,9 +308,9 @@ __global__ void __launch_bounds__(kThr) gen_dq_kernel(const __grid_constant__ Se
     if (flags[row] && i0 + row < n) fix_dq_row<E>(p, b, h, i0 + row);
 }
 
-template <typename E, int HD>
+template <typename E, int HD, int T>
 __global__ void __launch_bounds__(kThr) gen_dkv_kernel(const __grid_constant__ SeqParams p) {
-  constexpr int T = tile_of<HD>(), R = T / 16, NC = HD / 16;
+  constexpr int R = T / 16, NC = HD / 16;
   using C = Cols<HD>;
   extern __shared__ float sm[];
   float* ks = sm;
@@ -484,65 +482,64 @@ __global__ void __launch_bounds__(256) dkv_reduce_kernel(const __grid_constant__
   }
 }
 
-template <typename K>
-cudaError_t go(K kernel, long long grid, size_t smem, const SeqParams& p, cudaStream_t st) {
+template <auto Kernel>
+cudaError_t go(long long grid, size_t smem, const SeqParams& p, cudaStream_t st) {
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_smem<Kernel>(smem);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)grid, kThr, smem, st>>>(p);
+  Kernel<<<(unsigned)grid, kThr, smem, st>>>(p);
   note_launch();
   return cudaGetLastError();
 }
 
-template <typename E, int HD>
+template <typename E, int HD, int T>
 cudaError_t fwd(const SeqParams& p, cudaStream_t st) {
-  constexpr int T = tile_of<HD>();
   const size_t smem = (2 * T * (HD + 4) + T * (T + 4) + T) * 4;
-  return go(gen_fwd_kernel<E, HD>, (long long)p.B * p.H * ((p.S + T - 1) / T), smem, p, st);
+  return go<gen_fwd_kernel<E, HD, T>>((long long)p.B * p.H * ((p.S + T - 1) / T), smem, p, st);
 }
-template <typename E, int HD>
+template <typename E, int HD, int T>
 cudaError_t bwd(const SeqParams& p, cudaStream_t st) {
-  constexpr int T = tile_of<HD>();
   const size_t dq = (4 * T * (HD + 4) + T * (T + 4) + T) * 4;
   const size_t dkv = (4 * T * (HD + 4) + 2 * T * (T + 4) + 3 * T) * 4;
   const cudaError_t e =
-      go(gen_dq_kernel<E, HD>, (long long)p.B * p.H * ((p.S + T - 1) / T), dq, p, st);
+      go<gen_dq_kernel<E, HD, T>>((long long)p.B * p.H * ((p.S + T - 1) / T), dq, p, st);
   if (e != cudaSuccess) return e;
-  return go(gen_dkv_kernel<E, HD>, p.plan.items, dkv, p, st);
+  return go<gen_dkv_kernel<E, HD, T>>(p.plan.items, dkv, p, st);
+}
+template <typename E, int T>
+cudaError_t run_hd(const SeqParams& p, bool back, cudaStream_t st) {
+  if (p.hd <= 32) return back ? bwd<E, 32, T>(p, st) : fwd<E, 32, T>(p, st);
+  if (p.hd <= 64) return back ? bwd<E, 64, T>(p, st) : fwd<E, 64, T>(p, st);
+  return back ? bwd<E, 128, T>(p, st) : fwd<E, 128, T>(p, st);
 }
 template <typename E>
-cudaError_t fwd_hd(const SeqParams& p, cudaStream_t st) {
-  if (p.hd <= 32) return fwd<E, 32>(p, st);
-  if (p.hd <= 64) return fwd<E, 64>(p, st);
-  if (p.hd <= 128) return fwd<E, 128>(p, st);
-  return fwd<E, 256>(p, st);
-}
-template <typename E>
-cudaError_t bwd_hd(const SeqParams& p, cudaStream_t st) {
-  if (p.hd <= 32) return bwd<E, 32>(p, st);
-  if (p.hd <= 64) return bwd<E, 64>(p, st);
-  if (p.hd <= 128) return bwd<E, 128>(p, st);
-  return bwd<E, 256>(p, st);
+cudaError_t run_tile(const SeqParams& p, bool back, cudaStream_t st) {
+  if (p.hd > 128) return back ? bwd<E, 256, 32>(p, st) : fwd<E, 256, 32>(p, st);
+  return p.plan.T == 32 ? run_hd<E, 32>(p, back, st) : run_hd<E, 64>(p, back, st);
 }
 
 }  // namespace
 
-int seq_generic_tile(int hd) { return hd > 128 ? 32 : 64; }
+// 64 x 64 tiles feed the FMA pipe better, 32 x 32 tiles give four times the blocks;
+// the small ones are for work that would leave SMs without a block (and for heads
+// above 128, whose tiles would not fit shared memory).
+int seq_generic_tile(int B, int S, int H, int hd) {
+  return hd > 128 || (long long)B * H * ((S + 63) / 64) < kSeqSms ? 32 : 64;
+}
 
 DkvPlan make_dkv_plan(int B, int S, int K, int G, int hd, int window, int sinks, int T) {
   DkvPlan d;
   d.T = T;
   d.ntiles = (S + T - 1) / T;
-  // Chunks of the sink tiles' queries: about as many queries as a window tile
-  // has, 1024 at least and at most 16 chunks; not for more than four sink
-  // tiles, which are enough to fill the card by themselves.
+  // Chunks of the sink tiles' queries: as many queries as a window tile has, four
+  // tiles at least and at most 16 chunks; not for more than four sink tiles,
+  // which are enough to fill the card by themselves.
   const int st = (sinks + T - 1) / T;
   d.nst = d.qc = d.ch = 0;
   if (st > 0 && st <= 4) {
     int ch = (S + 15) / 16;
     ch = ch < window + T ? window + T : ch;
-    ch = ch < 1024 ? 1024 : ch;
+    ch = ch < 4 * T ? 4 * T : ch;
     ch = (int)(((long long)ch + T - 1) / T * T);
     if (ch < S) {
       d.nst = st < d.ntiles ? st : d.ntiles;
@@ -566,11 +563,13 @@ DkvPlan make_dkv_plan(int B, int S, int K, int G, int hd, int window, int sinks,
 }
 
 cudaError_t seq_generic_forward(const SeqParams& p, int dtype, cudaStream_t st) {
-  return dtype == SWIN_DTYPE_BF16 ? fwd_hd<__nv_bfloat16>(p, st) : fwd_hd<float>(p, st);
+  return dtype == SWIN_DTYPE_BF16 ? run_tile<__nv_bfloat16>(p, false, st)
+                                  : run_tile<float>(p, false, st);
 }
 
 cudaError_t seq_generic_backward(const SeqParams& p, int dtype, cudaStream_t st) {
-  return dtype == SWIN_DTYPE_BF16 ? bwd_hd<__nv_bfloat16>(p, st) : bwd_hd<float>(p, st);
+  return dtype == SWIN_DTYPE_BF16 ? run_tile<__nv_bfloat16>(p, true, st)
+                                  : run_tile<float>(p, true, st);
 }
 
 cudaError_t seq_prep(const SeqParams& p, int dtype, cudaStream_t st) {
