@@ -95,6 +95,11 @@ struct DecodePlan {
   long long vis_max;
 };
 
+// a / b, in 32 bits where both fit (a 64-bit division is some hundred cycles).
+__device__ __forceinline__ long long quot(long long a, long long b) {
+  return ((a | b) >> 32) ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 struct Vis {
   int n, len, first, shift;      // positions < first are themselves, others + shift
 };
@@ -175,9 +180,9 @@ __device__ __forceinline__ Place find_place(const CacheParams& p, int unit, int 
     pl.total += sh[w];
   }
   pl.total *= kcn;
-  pl.start = (long long)blockIdx.x * pl.total / C;
-  pl.end = (long long)(blockIdx.x + 1) * pl.total / C;
-  const long long target = pl.start / kcn;
+  pl.start = quot((long long)blockIdx.x * pl.total, C);
+  pl.end = quot((long long)(blockIdx.x + 1) * pl.total, C);
+  const long long target = quot(pl.start, kcn);
   long long before = inc - sum;
   if (pl.start < pl.end && target >= before && target < inc) {
     int b = b0;
@@ -249,18 +254,19 @@ __device__ __forceinline__ long long lane_row(const CacheParams& p, const Segmen
 }
 
 // bf16, head_dim 32, 64 or 128, 8 NT query heads of one kv head at a time. Each
-// warp runs alone over tiles of 32 positions through a ring of ST cp.async
-// stages (16-byte chunks, swizzled against bank conflicts). Logits transposed,
+// warp runs alone over tiles of TK positions through a ring of ST cp.async
+// stages (16-byte chunks, swizzled against bank conflicts); two blocks per SM, so
+// that one streams while the other ends a sequence. Logits transposed,
 // S^T = K Q^T, and O^T = V^T P^T, on mma.sync: the key and channel sides have
 // 16 rows to give and the query heads are the 8-wide side, so the eight heads
 // or fewer of a group fill a tile; P^T moves from the one product to the other
 // through movmatrix. Arithmetic is a few per cent of the warp's time: the
 // cache is read once, and its bytes bound the kernel.
-template <int HD, int NT, int ST>
+template <int HD, int NT, int ST, int TK>
 struct MmaCore {
-  static constexpr int kHeads = 8 * NT, kUnit = 128;   // 32 positions per warp
+  static constexpr int kHeads = 8 * NT, kUnit = 4 * TK;  // TK positions per warp and tile
   static constexpr int kCpr = HD / 8;                    // 16-byte chunks of a row
-  static constexpr int kTileBytes = 32 * HD * 2;         // one of K, V
+  static constexpr int kTileBytes = TK * HD * 2;         // one of K, V
   static constexpr int kWarpBytes = ST * 2 * kTileBytes + ST * 4;
   static constexpr size_t kRing = 4 * (size_t)((kWarpBytes + 127) / 128 * 128);
   static constexpr size_t kMerge = 4 * kHeads * (HD + 2) * sizeof(float);
@@ -306,22 +312,25 @@ struct MmaCore {
         for (int e = 0; e < 4; ++e) o[ct][nt][e] = 0.f;
     }
 
-    // tiles warp, warp + 4, ... of the segment's 32-position tiles
-    const int t_end = min(s.u1 * 4, (s.vis.n + 31) / 32);
+    // tiles warp, warp + 4, ... of the segment's TK-position tiles
+    const int t_end = min(s.u1 * 4, (s.vis.n + TK - 1) / TK);
     const int t0 = s.u0 * 4 + warp;
     const int cnt = t0 < t_end ? (t_end - t0 + 3) / 4 : 0;
-    long long row_next = cnt > 0 ? lane_row(p, s, t0 * 32 + lane) : -1;
+    auto row_of = [&](int tile) {   // lane r < TK: position r of the tile
+      return lane < TK ? lane_row(p, s, tile * TK + lane) : -1ll;
+    };
+    long long row_next = cnt > 0 ? row_of(t0) : -1;
     auto issue = [&](int x) {   // tile x of this warp into stage x % ST
       if (x < cnt) {
         const int st = x % ST;
         const long long row = row_next;
-        if (x + 1 < cnt) row_next = lane_row(p, s, (t0 + (x + 1) * 4) * 32 + lane);
+        if (x + 1 < cnt) row_next = row_of(t0 + (x + 1) * 4);
         const uint32_t ok = __ballot_sync(0xffffffffu, row != -1);
         if (lane == 0) vmask[st] = ok;
         const uint32_t kb = base + st * 2 * kTileBytes, vb = kb + kTileBytes;
         constexpr int RPI = 32 / kCpr;   // rows per instruction
 #pragma unroll
-        for (int i = 0; i < 32 / RPI; ++i) {
+        for (int i = 0; i < TK / RPI; ++i) {
           const int r = i * RPI + lane / kCpr, c = lane % kCpr;
           const long long rr = __shfl_sync(0xffffffffu, row, r);
           const __nv_bfloat16* ks = kc + (rr >= 0 ? rr : 0) * HD + c * 8;
@@ -345,9 +354,9 @@ struct MmaCore {
       const int st = x % ST;
       const uint32_t kb = base + st * 2 * kTileBytes, vb = kb + kTileBytes;
       const uint32_t ok = vmask[st];
-      float sacc[2][NT][4];
+      float sacc[TK / 16][NT][4];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
+      for (int mt = 0; mt < TK / 16; ++mt) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -360,12 +369,12 @@ struct MmaCore {
           for (int nt = 0; nt < NT; ++nt) mma16816(sacc[mt][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
         }
       }
-      uint32_t pf[2][NT][2];
+      uint32_t pf[TK / 16][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < TK / 16; ++mt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = mt * 16 + lane / 4 + (e >> 1) * 8;
@@ -374,9 +383,9 @@ struct MmaCore {
             mx[e & 1] = fmaxf(mx[e & 1], v);
           }
         if (d.logits) {
-          const int u = (t0 + x * 4) * 32;
+          const int u = (t0 + x * 4) * TK;
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+          for (int mt = 0; mt < TK / 16; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int key = mt * 16 + lane / 4 + (e >> 1) * 8;
@@ -403,7 +412,7 @@ struct MmaCore {
             for (int e = 0; e < 4; ++e) o[ct][nt][e] *= f[e & 1];
         }
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
+        for (int mt = 0; mt < TK / 16; ++mt) {
           float w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -417,7 +426,7 @@ struct MmaCore {
         }
       }
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+      for (int mt = 0; mt < TK / 16; ++mt)
 #pragma unroll
         for (int ct = 0; ct < HD / 16; ++ct) {
           uint32_t a[4];
@@ -592,7 +601,7 @@ __global__ void __launch_bounds__(kDecThr)
       ++b;
       continue;
     }
-    const int kc = (int)(rel / U);
+    const int kc = (int)quot(rel, U);
     s.kh = kc / d.nchunk;
     const int chunk = kc - s.kh * d.nchunk;
     s.h0 = s.kh * p.G + chunk * d.heads;
@@ -688,7 +697,7 @@ __global__ void __launch_bounds__(kJoinThr)
   }
   for (int chunk = 0; chunk < d.nchunk && U > 0; ++chunk) {
     const long long g0 = before * kcn + ((long long)kh * d.nchunk + chunk) * U, g1 = g0 + U;
-    const int c0 = (int)(((g0 + 1) * d.C - 1) / total), c1 = (int)((g1 * d.C - 1) / total);
+    const int c0 = (int)quot((g0 + 1) * d.C - 1, total), c1 = (int)quot(g1 * d.C - 1, total);
     const int h0 = chunk * d.heads, hc = min(d.heads, p.G - h0);   // within the group
     if (c0 == c1) {
       if (p.w_out)
@@ -699,7 +708,7 @@ __global__ void __launch_bounds__(kJoinThr)
     __syncthreads();
     for (int k = threadIdx.x; k < ns; k += kJoinThr) {
       const int c = c0 + k;
-      const long long s0 = c * total / d.C, s1 = (c + 1) * total / d.C;
+      const long long s0 = quot(c * total, d.C), s1 = quot((c + 1) * total, d.C);
       // a block without units has none of this; its first segment is in slot 0
       slots[k] = max(g0, s0) < min(g1, s1) ? 2 * c + (s0 >= g0 ? 0 : 1) : -1;
     }
@@ -733,15 +742,23 @@ __global__ void __launch_bounds__(kJoinThr)
       }
     }
     __syncthreads();
-    for (int x = blockIdx.y * kJoinThr + threadIdx.x; x < hc * p.hd; x += kJoinThr * gridDim.y) {
-      const int h = x / p.hd, c = x - h * p.hd;
+    // `lanes` neighbouring threads per output, each a part of the pieces (more where
+    // there are more threads than outputs)
+    const int all = hc * p.hd, threads = kJoinThr * gridDim.y;
+    int lanes = 1;
+    while (lanes < 32 && 2 * lanes * all <= threads) lanes *= 2;
+    const int sub = threadIdx.x & (lanes - 1);
+    for (int x0 = blockIdx.y * kJoinThr; x0 < all * lanes; x0 += threads) {
+      const int x = (x0 + (int)threadIdx.x) / lanes;
+      const int h = x < all ? x / p.hd : 0, c = x < all ? x - h * p.hd : 0;
       float O = 0.f;
-#pragma unroll 16
-      for (int k = 0; k < ns; ++k) {
+#pragma unroll 8
+      for (int k = sub; k < ns; k += lanes) {
         const float o = piece(k, h)[c];
         O = fmaf(slots[k] >= 0 ? o : 0.f, fac[h * d.C + k], O);
       }
-      seq_st((E*)p.out + (bh0 + h0 + h) * p.hd + c, O * inv_sh[h]);
+      for (int o = lanes / 2; o > 0; o >>= 1) O += __shfl_xor_sync(0xffffffffu, O, o);
+      if (x < all && sub == 0) seq_st((E*)p.out + (bh0 + h0) * p.hd + x, O * inv_sh[h]);
     }
   }
   if (!p.w_out) return;
@@ -1033,9 +1050,9 @@ DecodeShape decode_shape(const CacheParams& p, int dtype) {
   s.mma = dtype == SWIN_DTYPE_BF16 && (p.hd == 32 || p.hd == 64 || p.hd == 128);
   s.heads = s.mma ? (p.G <= 8 ? 8 : 16) : 4;
   s.nchunk = (p.G + s.heads - 1) / s.heads;
-  s.unit = s.mma ? 128 : (p.hd <= 64 ? 32 : 16);
+  s.unit = s.mma ? (p.hd == 128 ? 64 : 128) : (p.hd <= 64 ? 32 : 16);   // each Core's kUnit
   // blocks that fit the card at once (shared memory of the ring; registers)
-  const long long resident = (long long)kSeqSms * (s.mma ? (p.hd == 128 ? 1 : 2) : 4);
+  const long long resident = (long long)kSeqSms * (s.mma ? 2 : 4);
   const long long cap = (long long)p.window + p.sinks;
   const long long vis = p.max_len < cap ? p.max_len : cap;
   const long long most = (long long)p.B * p.K * s.nchunk * ((vis + s.unit - 1) / s.unit);
@@ -1077,11 +1094,18 @@ cudaError_t decode_go(const CacheParams& p, const DecodePlan& d, cudaStream_t st
   note_launch();
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  // a thread per output at least, eight where (b, kh) alone leave SMs idle
   const long long outs = ((long long)d.heads * p.hd + kJoinThr - 1) / kJoinThr;
   const long long spans = p.w_out ? (p.max_len + kJoinSpan - 1) / kJoinSpan : 1;
-  const unsigned pieces = (unsigned)(outs > spans ? outs : spans);
+  const long long spare = 2LL * kSeqSms / ((long long)p.B * p.K);
+  const long long wide = 8 * outs < spare ? 8 * outs : spare;
+  const long long most = outs > spans ? outs : spans;
+  const unsigned pieces = (unsigned)(most > wide ? most : wide);
   if (pieces > 65535) return cudaErrorInvalidConfiguration;
   const size_t smem = (size_t)(p.G + d.heads + d.C + 2 * d.heads * d.C) * 4;
+  // the split of L1 that decode_kernel runs with, so that blocks of both fit an SM
+  e = prefer_smem<join_kernel<E>>();
+  if (e != cudaSuccess) return e;
   return launch_dependent(join_kernel<E>, dim3(p.B * p.K, pieces), kJoinThr, smem, st, p, d);
 }
 
@@ -1096,9 +1120,9 @@ cudaError_t decode_lanes(const CacheParams& p, const DecodePlan& d, cudaStream_t
 template <int NT>
 cudaError_t decode_mma(const CacheParams& p, const DecodePlan& d, cudaStream_t st) {
   using E = __nv_bfloat16;
-  if (p.hd == 32) return decode_go<E, MmaCore<32, NT, 4>>(p, d, st);
-  if (p.hd == 64) return decode_go<E, MmaCore<64, NT, 3>>(p, d, st);
-  return decode_go<E, MmaCore<128, NT, 3>>(p, d, st);
+  if (p.hd == 32) return decode_go<E, MmaCore<32, NT, 4, 32>>(p, d, st);
+  if (p.hd == 64) return decode_go<E, MmaCore<64, NT, 3, 32>>(p, d, st);
+  return decode_go<E, MmaCore<128, NT, 3, 16>>(p, d, st);
 }
 
 }  // namespace

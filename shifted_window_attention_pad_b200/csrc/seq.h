@@ -44,6 +44,21 @@ cudaError_t allow_smem(size_t bytes) {
   return e;
 }
 
+// Runs `Kernel` with the largest shared-memory share of L1, once per device: so its
+// blocks can join those of a kernel that needs it on an SM.
+template <auto Kernel>
+cudaError_t prefer_smem() {
+  static std::atomic<uint64_t> done{0};   // by device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                           cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
+
 struct SeqParams {
   int B, S, H, K, G, hd;
   int window, sinks;               // window in 1 .. S; sinks 0 when the window hides nothing
