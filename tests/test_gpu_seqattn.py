@@ -55,6 +55,13 @@ CASES = [
     (1, 150, 2, 2, 8, 0, 0, None, False),
     (1, 130, 2, 1, 256, 33, 2, None, True),
     (2, 90, 2, 2, 136, 20, 0, [90, 64], False),
+    # enough heads for pairs of query tiles (and more items than SMs): lengths that end
+    # in either tile of a pair, windows and sinks whose key tiles only one tile needs
+    (2, 1100, 40, 10, 64, 0, 0, [1100, 769], False),
+    (2, 1100, 40, 40, 128, 200, 4, [1029, 896], False),
+    (3, 700, 32, 4, 64, 130, 70, [700, 513, 257], True),
+    (3, 700, 32, 32, 128, 64, 1, [640, 0, 129], False),
+    (5, 515, 32, 8, 32, 300, 0, [515, 385, 1, 256, 255], False),
 ]
 
 
@@ -232,6 +239,31 @@ def test_wrappers_refuse_what_the_description_does_not_say():
         sb.seq_forward(d, q, k, v, lengths=torch.tensor([4], device="cuda"))
     with pytest.raises(sb.SwinWattnError):
         sb.seq_forward(d, q, k, v, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_long_ragged_sequences_with_pairs_of_tiles(hd):
+    """Rounds of every ring many times over, lengths that leave the second tile of a
+    pair empty; sampled rows against the reference."""
+    S, H, window, sinks, lengths = 4096, 16, 512, 4, [3501, 1799, 2]
+    q, k, v, g = make(3, S, H, 4, hd, "bf16", seed=29)
+    got = run(q, k, v, g, window, sinks, lengths)
+    for b, n in enumerate(lengths):
+        for name in ALL:
+            assert not got[name][b, n:].any(), name
+        for h in (0, 5):
+            pick = lambda t, c: t[b:b + 1, :, c:c + 1]
+            want = ref.attention(pick(q, h), pick(k, h // 4), pick(v, h // 4), window, sinks, [n],
+                                 pick(g, h))
+            ref.check({x: got[x][b:b + 1, :, h:h + 1] for x in ("o", "lse", "dq")}, want,
+                      ("o", "lse", "dq"))
+        heads = range(4, 8)   # of kv head 1
+        parts = [ref.attention(pick(q, h), pick(k, 1), pick(v, 1), window, sinks, [n], pick(g, h))
+                 for h in heads]
+        for name in ("dk", "dv"):
+            ref_sum = sum(w[name][0] for w in parts)
+            bound = sum(w[name][1] for w in parts)
+            ref.check({name: got[name][b:b + 1, :, 1:2]}, {name: (ref_sum, bound)}, (name,))
 
 
 def test_one_row_sequences_in_a_large_batch():
