@@ -407,8 +407,10 @@ __global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ SeqPa
   bool real = false;
   long long at = -1;
   if (row < (long long)p.B * p.S * p.H) {
-    const long long tok = row / p.H;
-    const int h = (int)(row - tok * p.H), b = (int)(tok / p.S), i = (int)(tok - (long long)b * p.S);
+    // (32-bit division where it fits: a 64-bit one is some hundred cycles)
+    const long long tok = row >> 32 ? row / p.H : (long long)((uint32_t)row / (uint32_t)p.H);
+    const int h = (int)(row - tok * p.H);
+    const int b = (int)((uint32_t)tok / (uint32_t)p.S), i = (int)(tok - (long long)b * p.S);
     at = ((long long)b * p.H + h) * p.ld_stride + i;
     real = i < seq_len(p, b);
   }
@@ -532,14 +534,16 @@ DkvPlan make_dkv_plan(int B, int S, int K, int G, int hd, int window, int sinks,
   d.T = T;
   d.ntiles = (S + T - 1) / T;
   // Chunks of the sink tiles' queries: as many queries as a window tile has, four
-  // tiles at least and at most 16 chunks; not for more than four sink tiles,
-  // which are enough to fill the card by themselves.
+  // tiles at least (eight of the tensor-core kernels', whose items cost some steps
+  // besides) and at most 16 chunks; not for more than four sink tiles, which are
+  // enough to fill the card by themselves.
   const int st = (sinks + T - 1) / T;
   d.nst = d.qc = d.ch = 0;
   if (st > 0 && st <= 4) {
     int ch = (S + 15) / 16;
     ch = ch < window + T ? window + T : ch;
-    ch = ch < 4 * T ? 4 * T : ch;
+    const int least = T == 128 ? 8 * T : 4 * T;
+    ch = ch < least ? least : ch;
     ch = (int)(((long long)ch + T - 1) / T * T);
     if (ch < S) {
       d.nst = st < d.ntiles ? st : d.ntiles;

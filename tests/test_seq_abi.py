@@ -158,10 +158,9 @@ def test_workspace_grows_with_what_it_holds():
     one = sb.make_seq_desc(1, 256, 4, 64, 0, "bf16", kv_heads=1)
     assert sb.swin_seqattn_workspace_size(one) == 256 + a256(256 * 4 * 8) + 4 * 2 * 256 * 64 * 4
     sinks = sb.make_seq_desc(8, 4096, 32, 64, 512, "bf16", sinks=4)
-    # one sink tile of 128 keys for each of 8 x 32 heads, seven chunks of the 640
-    # queries that the tile's window reaches
+    # one sink tile of 128 keys for each of 8 x 32 heads, four chunks of 1024 queries
     assert (sb.swin_seqattn_workspace_size(sinks) - sb.swin_seqattn_workspace_size(d)
-            == 2 * 8 * 32 * 7 * 128 * 64 * 4)
+            == 2 * 8 * 32 * 4 * 128 * 64 * 4)
     # sinks that the window covers are no sinks
     wide = sb.make_seq_desc(8, 4096, 32, 64, 4096, "bf16", sinks=4)
     assert sb.swin_seqattn_workspace_size(wide) == sb.swin_seqattn_workspace_size(d)
