@@ -10,7 +10,9 @@
  * swin_wattn.h: every data pointer is device memory of the current device
  * owned by the caller, nothing is allocated, nothing is synchronised, and two
  * calls in flight at once must not share a workspace (calls, or captured
- * graphs, that follow one another on a stream may). Every call can be
+ * graphs, that follow one another on a stream may). The first 256 bytes of a
+ * workspace are zeroed by the caller once, before its first use: they hold the
+ * status word; the rest may hold anything. Every call can be
  * captured into a CUDA graph; lengths, counts and page tables are read on the
  * device when it runs.
  *

@@ -93,6 +93,7 @@ struct DecodePlan {
   float* lse2;                   // [B][H] of finished heads, log2 units
   float* logits;                 // weights: [B][H][vis_max], log2 units
   long long vis_max;
+  long long* prefix;             // [B + 1] units before each sequence; NULL: small batch
 };
 
 // a / b, in 32 bits where both fit (a 64-bit division is some hundred cycles).
@@ -149,6 +150,34 @@ __device__ __forceinline__ void batch_units(const CacheParams& p, int unit, int 
   __syncthreads();
 }
 
+// Units before every sequence of a batch that is too large for each block to add up
+// the lengths itself. One block; each thread a contiguous run, as in find_place.
+constexpr int kScanThr = 1024, kScanBatch = 1024;   // batches above take this kernel
+__global__ void __launch_bounds__(kScanThr)
+    units_scan_kernel(const __grid_constant__ CacheParams p, int unit, long long* prefix) {
+  __shared__ long long sh[32];
+  const int per = (p.B + kScanThr - 1) / kScanThr;
+  const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) sum += units_of(p, unit, b);
+  long long inc = sum;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  if (lane == 31) sh[warp] = inc;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) inc += sh[w];
+  long long at = inc - sum;
+  for (int b = b0; b < b1; ++b) {
+    prefix[b] = at;
+    at += units_of(p, unit, b);
+  }
+  if (threadIdx.x == kScanThr - 1) prefix[p.B] = inc;
+}
+
 // The block's place in the list of units: total units of the batch (per kv head and
 // chunk), and the sequence that holds unit `start / kcn` of block c's first unit
 // with the units before it. One pass over the lengths: each thread a contiguous run
@@ -157,8 +186,25 @@ struct Place {
   long long total, start, end, before;
   int b;
 };
-__device__ __forceinline__ Place find_place(const CacheParams& p, int unit, int C, int kcn,
-                                            long long* sh) {
+__device__ __forceinline__ Place find_place(const CacheParams& p, const DecodePlan& d, int unit,
+                                            int kcn, long long* sh) {
+  const int C = d.C;
+  if (d.prefix) {   // by bisection: the last sequence with prefix <= target
+    Place pl;
+    pl.total = d.prefix[p.B] * kcn;
+    pl.start = quot((long long)blockIdx.x * pl.total, C);
+    pl.end = quot((long long)(blockIdx.x + 1) * pl.total, C);
+    const long long target = quot(pl.start, kcn);
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int mid = lo + (hi - lo) / 2;
+      if (d.prefix[mid] <= target) lo = mid;
+      else hi = mid;
+    }
+    pl.b = lo;
+    pl.before = d.prefix[lo];
+    return pl;
+  }
   const int per = (p.B + kDecThr - 1) / kDecThr;
   const int b0 = threadIdx.x * per, b1 = min(p.B, b0 + per);
   long long sum = 0;
@@ -586,7 +632,7 @@ __global__ void __launch_bounds__(kDecThr)
   constexpr int kUnit = Core::kUnit;
   ptx::grid_dep_launch();   // join_kernel may start (and wait)
   const int kcn = p.K * d.nchunk, hw = p.hd + 2;
-  const Place pl = find_place(p, kUnit, d.C, kcn, sh);
+  const Place pl = find_place(p, d, kUnit, kcn, sh);
   long long cur = pl.start, before = pl.before;
   const long long start = pl.start, end = pl.end;
   int b = pl.b;
@@ -683,7 +729,12 @@ __global__ void __launch_bounds__(kJoinThr)
   const int b = blockIdx.x / p.K, kh = blockIdx.x - b * p.K;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   long long before, total;
-  batch_units<kJoinThr>(p, d.unit, b, sh, before, total);
+  if (d.prefix) {
+    before = d.prefix[b];
+    total = d.prefix[p.B];
+  } else {
+    batch_units<kJoinThr>(p, d.unit, b, sh, before, total);
+  }
   const int kcn = p.K * d.nchunk;
   total *= kcn;
   const Vis vis = vis_of(p, b);
@@ -1067,6 +1118,9 @@ size_t part_bytes(const CacheParams& p, const DecodeShape& s) {
   return align256((size_t)s.blocks * 2 * s.heads * (p.hd + 2) * 4);
 }
 size_t lse_bytes(const CacheParams& p) { return align256((size_t)p.B * p.H * 4); }
+size_t prefix_bytes(const CacheParams& p) {
+  return p.B > kScanBatch ? align256(((size_t)p.B + 1) * 8) : 0;
+}
 
 template <typename K, typename... A>
 cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st,
@@ -1131,7 +1185,7 @@ cudaError_t decode_mma(const CacheParams& p, const DecodePlan& d, cudaStream_t s
 // kept positions of evict: the calls share the space.
 size_t cache_workspace(const CacheParams& p, int dtype) {
   const DecodeShape s = decode_shape(p, dtype);
-  const size_t dec = part_bytes(p, s) + lse_bytes(p) +
+  const size_t dec = part_bytes(p, s) + lse_bytes(p) + prefix_bytes(p) +
                      (p.with_weights ? align256((size_t)p.B * p.H * vis_max(p) * 4) : 0);
   const size_t evict = align256((size_t)p.B * p.K * p.budget * 4);
   return dec > evict ? dec : evict;
@@ -1161,8 +1215,16 @@ cudaError_t cache_decode(const CacheParams& p, int dtype, cudaStream_t st) {
   d.hds = p.hd + 2;
   d.part = (float*)p.ws;
   d.lse2 = (float*)(p.ws + part_bytes(p, s));
-  d.logits = p.w_out ? (float*)(p.ws + part_bytes(p, s) + lse_bytes(p)) : nullptr;
+  char* rest = p.ws + part_bytes(p, s) + lse_bytes(p);
+  d.prefix = p.B > kScanBatch ? (long long*)rest : nullptr;
+  d.logits = p.w_out ? (float*)(rest + prefix_bytes(p)) : nullptr;
   d.vis_max = vis_max(p);
+  if (d.prefix) {
+    units_scan_kernel<<<1, kScanThr, 0, st>>>(p, s.unit, d.prefix);
+    note_launch();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   if (s.mma) return s.heads == 8 ? decode_mma<1>(p, d, st) : decode_mma<2>(p, d, st);
   return dtype == SWIN_DTYPE_BF16 ? decode_lanes<__nv_bfloat16>(p, d, st)
                                   : decode_lanes<float>(p, d, st);

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(BwdTmem<HD, KEYS>::kThreads, 1)
     for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
     mbar_init(never, 1);
     feed_init(feed, 2 + kSoft);   // the MMA and softmax warps
-    *abort = 0;
+    abort[0] = abort[1] = 0;   // [1]: warps that recompute rows
     fence_mbar_init();
   }
   if (warp == kBProducer && lane == 0) {
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(BwdTmem<HD, KEYS>::kThreads, 1)
       __syncwarp();
       ra.next();
     }
-    if (*abort && lane == 0) {
+    if (__any_sync(0xffffffffu, *abort) && elect_one()) {   // the lane that issued
       umma_commit(&drain[0]);
       mbar_drain(&drain[0], 0, kTestLimitNs * 100);
     }
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(BwdTmem<HD, KEYS>::kThreads, 1)
       __syncwarp();
       acc.next();
     }
-    if (*abort && lane == 0) {
+    if (__any_sync(0xffffffffu, *abort) && elect_one()) {
       umma_commit(&drain[1]);
       mbar_drain(&drain[1], 0, kTestLimitNs * 100);
     }
@@ -605,6 +605,8 @@ __global__ void __launch_bounds__(BwdTmem<HD, KEYS>::kThreads, 1)
         // an item without steps has no products: its rows are zeros whatever TMEM holds
         bad = store_grad<NC>(acc, mul, real && it.steps, dst, f32, p.hd - (KEYS ? 0 : wg * NC),
                              it.steps ? &acc_empty[racc.s] : nullptr) && real && it.steps;
+        // (a row whose L or D is NaN has a NaN of its own: it is as it should be)
+        if (!KEYS && !(nl == nl && nd == nd)) bad = false;
       }
       if (it.steps) racc.next();
       if (named_sync_or(1, kSoft * 32, bad && !*abort)) {
@@ -612,12 +614,14 @@ __global__ void __launch_bounds__(BwdTmem<HD, KEYS>::kThreads, 1)
         if (wg == 0) flags[row] = 0;
         named_sync(1, kSoft * 32);
         if (bad) flags[row] = 1;
+        if (lane == 0) atomicAdd((int*)abort + 1, 1);
         named_sync(1, kSoft * 32);
         for (int y = warp; y < kRows; y += kSoft)
           if (flags[y]) {
             if constexpr (KEYS) fix_dkv_row<__nv_bfloat16>(p, it.d, it.r0 + y);
             else fix_dq_row<__nv_bfloat16>(p, it.b, it.h, it.r0 + y);
           }
+        if (lane == 0) atomicAdd((int*)abort + 1, -1);
         named_sync(1, kSoft * 32);
       }
     }

@@ -139,6 +139,16 @@ __device__ __forceinline__ void fix_store(E* row, const float* r, float mul, int
     if (lane + 32 * t < hd) seq_st(row + lane + 32 * t, r[t] * mul);
 }
 
+// Every channel of both is NaN already (all lanes agree): nothing can change it.
+__device__ __forceinline__ bool fix_lost(const float* a, const float* b, int hd) {
+  bool lost = true;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int t = 0; t < kFixT; ++t)
+    if (lane + 32 * t < hd) lost &= a[t] != a[t] && b[t] != b[t];
+  return __all_sync(0xffffffffu, lost);
+}
+
 template <typename E>
 __device__ __noinline__ void fix_out_row(const SeqParams& p, int b, int h, int i) {
   const int kh = h / p.G;
@@ -162,6 +172,8 @@ __device__ __noinline__ void fix_out_row(const SeqParams& p, int b, int h, int i
     fix_load(x, vb + (long long)j * p.ks, p.hd);
 #pragma unroll
     for (int t = 0; t < kFixT; ++t) acc[t] = fmaf(w, x[t], acc[t] * f);
+    // (lse needs every key: only where it is NaN as well is there nothing left)
+    if ((j & 15) == 15 && l != l && fix_lost(acc, acc, p.hd)) break;
   }
   const long long row = ((long long)b * p.S + i) * p.H + h;
   fix_store((E*)p.out + row * p.hd, acc, 1.f / l, p.hd);
@@ -189,6 +201,7 @@ __device__ __noinline__ void fix_dq_row(const SeqParams& p, int b, int h, int i)
     const float ds = w * (fix_dot(g, y) + nd);
 #pragma unroll
     for (int t = 0; t < kFixT; ++t) acc[t] = fmaf(ds, x[t], acc[t]);
+    if ((j & 15) == 15 && fix_lost(acc, acc, p.hd)) break;
   }
   fix_store((E*)p.dq + ((long long)b * p.S + i) * p.qs + (long long)h * p.hd, acc, p.scale, p.hd);
 }
@@ -203,8 +216,9 @@ __device__ __noinline__ void fix_dkv_row(const SeqParams& p, const DkvItem& it, 
   fix_load(v, (const E*)p.v + at, p.hd);
 #pragma unroll
   for (int t = 0; t < kFixT; ++t) ak[t] = av[t] = 0.f;
-  for (int h = it.h0; h < it.h1; ++h)
-    for (int i = max(it.i0, j); i < it.i1; ++i) {
+  bool lost = false;
+  for (int h = it.h0; h < it.h1 && !lost; ++h)
+    for (int i = max(it.i0, j); i < it.i1 && !lost; ++i) {
       if (!seq_visible(p, it.n, i, j)) break;
       fix_load(x, (const E*)p.q + ((long long)it.b * p.S + i) * p.qs + (long long)h * p.hd, p.hd);
       fix_load(y, (const E*)p.dout + (((long long)it.b * p.S + i) * p.H + h) * p.hd, p.hd);
@@ -216,6 +230,7 @@ __device__ __noinline__ void fix_dkv_row(const SeqParams& p, const DkvItem& it, 
         ak[t] = fmaf(ds, x[t], ak[t]);
         av[t] = fmaf(w, y[t], av[t]);
       }
+      lost = (i & 15) == 15 && fix_lost(ak, av, p.hd);
     }
   if (it.partial) {
     const long long r = (j - it.tile * p.plan.T) * it.row_stride;

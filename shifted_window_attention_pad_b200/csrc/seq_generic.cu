@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(kThr) gen_dq_kernel(const __grid_constant__ Se
     if (row >= stored) continue;
 #pragma unroll
     for (int c = 0; c < NC; ++c)
-      if (C::col(tx, c) < p.hd) seq_st(dq + row * p.qs + C::col(tx, c), acc[r][c] * p.scale);
+      if (C::col(tx, c) < p.hd)   // padding: zeros, whatever masked tokens hold
+        seq_st(dq + row * p.qs + C::col(tx, c), i0 + row < n ? acc[r][c] * p.scale : 0.f);
   }
   flag_rows<R, NC>(acc, flags, ty);
   __syncthreads();
@@ -378,12 +379,14 @@ __global__ void __launch_bounds__(kThr) gen_dkv_kernel(const __grid_constant__ S
     for (int c = 0; c < NC; ++c) {
       const int col = C::col(tx, c);
       if (col >= p.hd) continue;
+      const bool real = j0 + row < it.n;   // padding: zeros, whatever masked tokens hold
+      const float dk = real ? ak[r][c] * p.scale : 0.f, dv = real ? av[r][c] : 0.f;
       if (it.partial) {
-        it.pk[row * it.row_stride + col] = ak[r][c] * p.scale;
-        it.pv[row * it.row_stride + col] = av[r][c];
+        it.pk[row * it.row_stride + col] = dk;
+        it.pv[row * it.row_stride + col] = dv;
       } else {
-        seq_st((E*)p.dk + at + col, ak[r][c] * p.scale);
-        seq_st((E*)p.dv + at + col, av[r][c]);
+        seq_st((E*)p.dk + at + col, dk);
+        seq_st((E*)p.dv + at + col, dv);
       }
     }
   }

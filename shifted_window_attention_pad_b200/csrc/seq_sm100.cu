@@ -93,7 +93,7 @@ struct SeqFwdCfg {
   static constexpr uint32_t kBars = kRing + kSlots * kSlot;
   static constexpr int kNumBars = 2 * kQBufs + 2 * kSlots + 6 * NB + 2 + 2 + 1;
   static constexpr uint32_t kFeedAt = kBars + (kNumBars * 8 + 15) / 16 * 16;
-  static constexpr uint32_t kTotal = kFeedAt + sizeof(Feed<SeqItem<KT>>) + 16;
+  static constexpr uint32_t kTotal = kFeedAt + sizeof(Feed<SeqItem<KT>>) + 16;   // TMEM address, abort
   static constexpr uint32_t kSmem = kTotal + 1024;
 };
 
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
     for (int i = 0; i < 2; ++i) { mbar_init(&o_empty[i], kWg); mbar_init(&drain[i], 1); }
     mbar_init(never, 1);
     feed_init(feed, 2 + 8);   // the MMA and softmax warps
-    *abort = 0;
+    abort[0] = abort[1] = 0;   // [1]: warps that recompute rows
     fence_mbar_init();
   }
   if (warp == kSeqProducer && lane == 0) {
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
       __syncwarp();
       rq.next();
     }
-    if (*abort && lane == 0) {
+    if (__any_sync(0xffffffffu, *abort) && elect_one()) {   // the lane that issued
       umma_commit(&drain[0]);
       mbar_drain(&drain[0], 0, kTestLimitNs * 100);
     }
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
 #pragma unroll
       for (int w = 0; w < 2; ++w) items[w] += it.has[w];
     }
-    if (*abort && lane == 0) {
+    if (__any_sync(0xffffffffu, *abort) && elect_one()) {
       umma_commit(&drain[1]);
       mbar_drain(&drain[1], 0, kTestLimitNs * 100);
     }
@@ -470,12 +470,18 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
         store_rows_clipped<8>(a, stored && live ? dst + c : nullptr, (p.hd - c) / 8);
       }
       if (stored && live && p.lse) p.lse[orow] = real ? (m + __log2f(l)) / kSeqLog2e : 0.f;
-      uint32_t fix = __ballot_sync(0xffffffffu, bad && real && live);
-      while (fix) {
-        const int r = __ffs(fix) - 1;
-        fix &= fix - 1;
+      // a row whose sum is NaN has a NaN logit of its own: it is as it should be
+      uint32_t fix = __ballot_sync(0xffffffffu, bad && real && live && l == l);
+      if (fix) {
+        if (lane == 0) atomicAdd((int*)abort + 1, 1);
+        while (fix) {
+          const int r = __ffs(fix) - 1;
+          fix &= fix - 1;
+          __syncwarp();
+          fix_out_row<__nv_bfloat16>(p, it.b, it.h, i0 + (warp & 3) * 32 + r);
+        }
         __syncwarp();
-        fix_out_row<__nv_bfloat16>(p, it.b, it.h, i0 + (warp & 3) * 32 + r);
+        if (lane == 0) atomicAdd((int*)abort + 1, -1);
       }
     }
   }

@@ -9,14 +9,28 @@ namespace swin {
 namespace {
 
 // ---- waits -----------------------------------------------------------------------
-// Bounded as mbar_wait is, but the clock is read only after a number of tries (a
-// read costs more than a product's wait usually lasts).
+// Bounded as mbar_wait is; the clock is read only after a number of tries (a read
+// costs more than a product's wait usually lasts), and time in which softmax warps
+// recompute rows (abort[1], see fix_out_row) does not count.
 __device__ __forceinline__ bool seq_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                          int* status) {
 #pragma unroll 1
   for (int i = 0; i < 64; ++i)
     if (ptx::mbar_try_wait(bar, parity)) return true;
-  return ptx::mbar_wait(bar, parity, abort, status, kWaitLimitNs);
+  uint64_t t0 = ptx::globaltimer();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (ptx::mbar_try_wait(bar, parity)) return true;
+    if (abort[0]) return false;
+    const uint64_t now = ptx::globaltimer();
+    if (abort[1]) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
+      abort[0] = 1;
+      atomicExch(status, SWIN_ERR_TIMEOUT);
+      return false;
+    }
+  }
 }
 // A wait of a whole warp: every lane sees the phase, and all take the same way
 // when the wait is given up.

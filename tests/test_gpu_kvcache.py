@@ -129,6 +129,24 @@ def test_decode_of_many_ragged_sequences():
     finite({"o": out, "lse": lse}, want, ("o", "lse"))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_of_a_batch_of_thousands(dtype):
+    """More sequences than a block adds up itself, most of them short."""
+    B = 2500
+    lengths = [(b * 7919) % 40 if b % 100 else 150 + b // 10 for b in range(B)]
+    c = Cache(B, 2, 1, 64, 16, 26, dtype, lengths, seed=3, weights=True)
+    q = c.new(B, 2)
+    w = torch.rand(B, 1, 26 * 16, generator=c.gen, device="cuda")
+    nw = w.clone()
+    out, lse = sb.cache_decode(c.desc, q, c.lengths, c.table, c.k, c.v, weights=w, new_weights=nw,
+                               want_lse=True, workspace=c.ws)
+    assert c.status() == 0
+    pick = [0, 1, 2, 99, 100, 1023, 1024, 1025, 2300, 2400, 2499]
+    at = torch.tensor(pick, device="cuda")
+    want = ref.decode(q[at], c.k, c.v, c.table[at], [lengths[b] for b in pick], 16, 0, 0, w[at])
+    finite({"o": out[at], "lse": lse[at], "weights": nw[at]}, want, ("o", "lse", "weights"))
+
+
 def test_decode_takes_parts_of_one_projection():
     lengths = [200, 90]
     c = Cache(2, 8, 2, 64, 16, 20, "bf16", lengths, seed=4, q_stride=12 * 64, kv_stride=12 * 64)

@@ -9,6 +9,7 @@ from shifted_window_attention_pad_b200 import binding as sb
 
 pytestmark = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+NAN = float("nan")
 
 
 def make(B, S, H, K, hd, dtype, seed=0, fused=False):
@@ -138,6 +139,26 @@ def test_a_nan_reaches_only_the_rows_that_see_it(dtype, hd):
     ref.check(clean(got, others), cut(want, others), ("dq",))
 
 
+@pytest.mark.parametrize("dtype,hd", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("which", ["q", "k", "v", "g", "all"])
+def test_tensors_of_nan(which, dtype, hd):
+    """A whole tensor of NaN (a run that has diverged): every row that sees one is
+    NaN, and the call ends with its status in order."""
+    t = dict(zip("qkvg", make(2, 700, 8, 4, hd, dtype, seed=31)))
+    for name in t:
+        if which in (name, "all"):
+            t[name].fill_(NAN)
+    got = run(t["q"], t["k"], t["v"], t["g"], 300, 2, [700, 401])
+    for b, n in enumerate((700, 401)):
+        for name in ("dq", "dk", "dv"):
+            # dO does not meet V or Q in dV, P does not meet V
+            if not (name == "dv" and which == "v"):
+                assert torch.isnan(got[name][b, :n]).all(), name
+            assert not got[name][b, n:].any(), name
+        assert torch.isnan(got["o"][b, :n]).all() == (which != "g")
+        assert torch.isfinite(got["o"][b, :n]).all() == (which == "g")
+
+
 @pytest.mark.parametrize("dtype,hd", [("bf16", 64), ("f32", 64)])
 def test_lengths_out_of_range_count_as_the_bounds(dtype, hd):
     q, k, v, g = make(2, 140, 2, 2, hd, dtype, seed=11)
@@ -220,9 +241,11 @@ def test_timeouts_are_reported():
     q, k, v, g = make(1, 200, 2, 2, 64, "bf16", seed=25)
     d = sb.seq_desc_for(q, k, window=0, flags=sb.SWIN_FLAG_TEST_TIMEOUT)
     ws = sb.new_seq_workspace(d)
-    sb.seq_forward(d, q, k, v, workspace=ws)
+    out, lse = sb.seq_forward(d, q, k, v, want_lse=True, workspace=ws)
     assert sb.swin_wattn_poll_status(ws) == sb.SWIN_ERR_TIMEOUT
     assert sb.swin_wattn_poll_status(ws) == 0
+    sb.seq_backward(d, q, k, v, out.zero_(), lse.zero_(), g, workspace=ws)
+    assert sb.swin_wattn_poll_status(ws) == sb.SWIN_ERR_TIMEOUT
     ref.check(run(q, k, v, g, 0, 0, ws=ws), ref.attention(q, k, v, 0, 0, None, g), ALL)
 
 
