@@ -12,11 +12,8 @@ namespace {
 // Bounded as mbar_wait is; the clock is read only after a number of tries (a read
 // costs more than a product's wait usually lasts), and time in which softmax warps
 // recompute rows (abort[1], see fix_out_row) does not count.
-__device__ __forceinline__ bool seq_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                         int* status) {
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (ptx::mbar_try_wait(bar, parity)) return true;
+__device__ __noinline__ bool seq_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                           int* status) {
   uint64_t t0 = ptx::globaltimer();
   for (;;) {
 #pragma unroll 1
@@ -31,6 +28,13 @@ __device__ __forceinline__ bool seq_wait(uint64_t* bar, uint32_t parity, volatil
       return false;
     }
   }
+}
+__device__ __forceinline__ bool seq_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                         int* status) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+  return seq_wait_long(bar, parity, abort, status);
 }
 // A wait of a whole warp: every lane sees the phase, and all take the same way
 // when the wait is given up.
