@@ -14,6 +14,9 @@ namespace {
 // recompute rows (abort[1], see fix_out_row) does not count.
 __device__ __noinline__ bool seq_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort,
                                            int* status) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (ptx::mbar_try_wait(bar, parity)) return true;
   uint64_t t0 = ptx::globaltimer();
   for (;;) {
 #pragma unroll 1
@@ -31,9 +34,7 @@ __device__ __noinline__ bool seq_wait_long(uint64_t* bar, uint32_t parity, volat
 }
 __device__ __forceinline__ bool seq_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                          int* status) {
-#pragma unroll 1
-  for (int i = 0; i < 64; ++i)
-    if (ptx::mbar_try_wait(bar, parity)) return true;
+  if (ptx::mbar_try_wait(bar, parity)) return true;
   return seq_wait_long(bar, parity, abort, status);
 }
 // A wait of a whole warp: every lane sees the phase, and all take the same way
