@@ -413,10 +413,10 @@ def _device_of(t, name):
 
 def _dense(t, name, dtype, shape, dev):
     """Address of a contiguous tensor of this type and shape."""
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape
-            or t.get_device() != dev or not t.is_contiguous()):
-        _refuse(t, name, dtype, shape, dev)
-    return t.data_ptr()
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+            and t.is_contiguous() and t.get_device() == dev):
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, dev)
 
 
 def _maybe(t, name, dtype, shape, dev):
@@ -426,19 +426,20 @@ def _maybe(t, name, dtype, shape, dev):
 def _tokens(t, name, dtype, shape, stride, dev):
     """Address of [B, T, heads, hd] or [B, heads, hd] with tokens `stride` elements
     apart (0: contiguous)."""
-    if not stride:
-        if (isinstance(t, torch.Tensor) and t.shape == shape and not t.is_contiguous()):
-            raise ValueError("%s has strides %s, the description says contiguous"
-                             % (name, t.stride()))
-        return _dense(t, name, dtype, shape, dev)
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape
-            or t.get_device() != dev):
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+            and t.get_device() == dev):
         _refuse(t, name, dtype, shape, dev)
-    want = (shape[1] * stride, stride) if len(shape) == 4 else (stride,)
-    for n, have, need in zip(shape, t.stride(), want + (shape[-1], 1)):
-        if n > 1 and have != need:
-            raise ValueError("%s has strides %s, the description says %d between tokens"
-                             % (name, t.stride(), stride))
+    if not stride:
+        if t.is_contiguous():
+            return t.data_ptr()
+        raise ValueError("%s has strides %s, the description says contiguous" % (name, t.stride()))
+    want = ((shape[1] * stride, stride) if len(shape) == 4 else (stride,)) + (shape[-1], 1)
+    have = t.stride()
+    if have != want:   # a dimension of one entry has no stride
+        for n, x, y in zip(shape, have, want):
+            if n > 1 and x != y:
+                raise ValueError("%s has strides %s, the description says %d between tokens"
+                                 % (name, have, stride))
     return t.data_ptr()
 
 
@@ -538,7 +539,7 @@ def swin_seqattn_bwd(desc, q, k, v, lengths, out, lse, dout, dq, dk, dv, workspa
 
 def seq_forward(desc, q, k, v, lengths=None, want_lse=False, workspace=None):
     sq, _, sl = _seq_shapes(desc)
-    out = q.new_empty(sq)
+    out = q.new_empty(sq) if desc.q_stride else torch.empty_like(q)
     lse = q.new_empty(sl, dtype=torch.float32) if want_lse else None
     swin_seqattn_fwd(desc, q, k, v, lengths, out, lse, workspace)
     return (out, lse) if want_lse else out
@@ -548,14 +549,14 @@ def seq_backward(desc, q, k, v, out, lse, dout, lengths=None, workspace=None):
     """dq, dk, dv, laid out as the description lays out q, k and v: parts of one
     [B, S, heads + 2 kv_heads, hd] buffer when its strides are that buffer's."""
     B, S, H, K, hd = desc.B, desc.S, desc.heads, desc.kv_heads, desc.head_dim
-    new = lambda n: q.new_empty((B, S, n, hd))
     if desc.q_stride and desc.q_stride == desc.kv_stride == (H + 2 * K) * hd:
-        both = new(H + 2 * K)
+        both = q.new_empty((B, S, H + 2 * K, hd))
         dq, dk, dv = both[:, :, :H], both[:, :, H:H + K], both[:, :, H + K:]
     else:
-        wide = lambda n, s: (new(n) if not s else
-                             q.new_empty((B, S, s))[:, :, :n * hd].unflatten(2, (n, hd)))
-        dq, dk, dv = wide(H, desc.q_stride), wide(K, desc.kv_stride), wide(K, desc.kv_stride)
+        wide = lambda t, n, s: (torch.empty_like(t) if not s else
+                                q.new_empty((B, S, s))[:, :, :n * hd].unflatten(2, (n, hd)))
+        dq = wide(q, H, desc.q_stride)
+        dk, dv = wide(k, K, desc.kv_stride), wide(v, K, desc.kv_stride)
     return swin_seqattn_bwd(desc, q, k, v, lengths, out, lse, dout, dq, dk, dv, workspace)
 
 
@@ -635,7 +636,8 @@ def cache_decode(desc, q, lengths, page_table, k_cache, v_cache, k_new=None, v_n
                  weights=None, new_weights=None, want_lse=False, workspace=None):
     """Attention of one token per sequence, q [B, heads, hd], over the cache.
     With `weights` and no new_weights the step's weights are added in place."""
-    out = q.new_empty((desc.B, desc.heads, desc.head_dim))
+    out = (q.new_empty((desc.B, desc.heads, desc.head_dim)) if desc.q_stride
+           else torch.empty_like(q))
     lse = q.new_empty((desc.B, desc.heads), dtype=torch.float32) if want_lse else None
     if weights is not None and new_weights is None:
         new_weights = weights

@@ -1122,24 +1122,6 @@ size_t prefix_bytes(const CacheParams& p) {
   return p.B > kScanBatch ? align256(((size_t)p.B + 1) * 8) : 0;
 }
 
-template <typename K, typename... A>
-cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st,
-                             A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  if (e == cudaSuccess) note_launch();
-  return e;
-}
-
 template <typename E, class Core>
 cudaError_t decode_go(const CacheParams& p, const DecodePlan& d, cudaStream_t st) {
   cudaError_t e = allow_smem<decode_kernel<E, Core>>(Core::kSmem);

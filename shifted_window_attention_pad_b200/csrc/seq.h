@@ -31,6 +31,27 @@ struct DkvPlan {
   size_t main_bytes, sink_bytes;   // partials of dk and dv together
 };
 
+// Launches a kernel as a programmatic dependent of the one before it on the stream:
+// its blocks may start while that one ends, and wait (grid_dep_wait) before they
+// touch what it wrote.
+template <typename K, typename... A>
+cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t st,
+                             A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
 // Lets `Kernel` use `bytes` of dynamic shared memory, once per device.
 template <auto Kernel>
 cudaError_t allow_smem(size_t bytes) {

@@ -253,6 +253,10 @@ __global__ void __launch_bounds__(BwdTmem<HD, KEYS>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // up to here the kernel before this one may still run; the next one's blocks may
+  // set themselves up behind this one's in the same way
+  grid_dep_wait();
+  grid_dep_launch();
   FeedRead<Item> rd{feed};
 
   if (warp == kBProducer) {
@@ -643,9 +647,8 @@ cudaError_t bwd_launch(const SeqParams& p, const BwdMaps& maps, cudaStream_t st)
   const long long items =
       KEYS ? p.plan.items : (long long)p.B * p.H * ((p.S + kRows - 1) / kRows);
   if (items > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  seq_bwd_kernel<HD, KEYS><<<(unsigned)items, BwdTmem<HD, KEYS>::kThreads, C::kSmem, st>>>(p, maps);
-  note_launch();
-  return cudaGetLastError();
+  return launch_dependent(seq_bwd_kernel<HD, KEYS>, dim3((unsigned)items),
+                          BwdTmem<HD, KEYS>::kThreads, C::kSmem, st, p, maps);
 }
 
 }  // namespace

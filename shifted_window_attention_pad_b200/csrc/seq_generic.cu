@@ -14,6 +14,7 @@
 #include <math.h>
 
 #include "seq_common.cuh"
+#include "sm100_ptx.cuh"
 
 namespace swin {
 namespace {
@@ -251,6 +252,7 @@ __global__ void __launch_bounds__(kThr) gen_dq_kernel(const __grid_constant__ Se
   const int b = (int)(bh / p.H), h = (int)(bh - (long long)b * p.H), kh = h / p.G;
   const int n = seq_len(p, b), i0 = tile * T, stored = min(T, p.S - i0);
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  ptx::grid_dep_wait();
   float acc[R][NC];
   float2 ld[R];
 #pragma unroll
@@ -323,6 +325,7 @@ __global__ void __launch_bounds__(kThr) gen_dkv_kernel(const __grid_constant__ S
   float2* lds = (float2*)(ds + T * (T + 4));
   int* flags = (int*)(lds + T);
   const DkvItem it = dkv_item(p, blockIdx.x);
+  ptx::grid_dep_wait();
   const int j0 = it.tile * T, stored = min(T, p.S - j0);
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   float ak[R][NC], av[R][NC];
@@ -402,6 +405,9 @@ __global__ void __launch_bounds__(kThr) gen_dkv_kernel(const __grid_constant__ S
 // Bound by HBM (out and dout once).
 template <typename E>
 __global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ SeqParams p, int lanes) {
+  // (only blocks that fill an SM may come early: small ones would crowd on the first
+  // SMs with room, 80 us against 65 for the portable backward of 544 tokens)
+  if (p.plan.T == 128) ptx::grid_dep_launch();
   const int per = 256 / lanes;
   const long long row = (long long)blockIdx.x * per + threadIdx.x / lanes;   // (b S + i) H + h
   const int lane = threadIdx.x % lanes;
@@ -447,11 +453,12 @@ __global__ void __launch_bounds__(256) dkv_reduce_kernel(const __grid_constant__
   const uint32_t rows = d.gs > 1 ? p.S : min(p.S, d.nst * d.T);
   const uint32_t per = p.K * q4;   // of a token
   const long long tok = x / per;
-  if (tok >= (long long)p.B * rows) return;
+  if (tok >= (long long)p.B * rows) return;   // (nothing to wait for)
   const uint32_t y = (uint32_t)(x - tok * per);
   const int kh = y / q4, c = (int)(y - kh * q4) * 4;
   const int b = (int)((uint32_t)tok / rows), j = (int)((uint32_t)tok - b * rows);
   const int tile = j / d.T;
+  ptx::grid_dep_wait();
   float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
   auto add = [](float4& a, const float* s) {
     const float4 t = *reinterpret_cast<const float4*>(s);
@@ -487,11 +494,13 @@ __global__ void __launch_bounds__(256) dkv_reduce_kernel(const __grid_constant__
   }
 }
 
+// `after`: behind another kernel of the same call.
 template <auto Kernel>
-cudaError_t go(long long grid, size_t smem, const SeqParams& p, cudaStream_t st) {
+cudaError_t go(long long grid, size_t smem, const SeqParams& p, cudaStream_t st, bool after) {
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const cudaError_t e = allow_smem<Kernel>(smem);
   if (e != cudaSuccess) return e;
+  if (after) return launch_dependent(Kernel, dim3((unsigned)grid), kThr, smem, st, p);
   Kernel<<<(unsigned)grid, kThr, smem, st>>>(p);
   note_launch();
   return cudaGetLastError();
@@ -500,16 +509,17 @@ cudaError_t go(long long grid, size_t smem, const SeqParams& p, cudaStream_t st)
 template <typename E, int HD, int T>
 cudaError_t fwd(const SeqParams& p, cudaStream_t st) {
   const size_t smem = (2 * T * (HD + 4) + T * (T + 4) + T) * 4;
-  return go<gen_fwd_kernel<E, HD, T>>((long long)p.B * p.H * ((p.S + T - 1) / T), smem, p, st);
+  return go<gen_fwd_kernel<E, HD, T>>((long long)p.B * p.H * ((p.S + T - 1) / T), smem, p, st,
+                                      false);
 }
 template <typename E, int HD, int T>
 cudaError_t bwd(const SeqParams& p, cudaStream_t st) {
   const size_t dq = (4 * T * (HD + 4) + T * (T + 4) + T) * 4;
   const size_t dkv = (4 * T * (HD + 4) + 2 * T * (T + 4) + 3 * T) * 4;
   const cudaError_t e =
-      go<gen_dq_kernel<E, HD, T>>((long long)p.B * p.H * ((p.S + T - 1) / T), dq, p, st);
+      go<gen_dq_kernel<E, HD, T>>((long long)p.B * p.H * ((p.S + T - 1) / T), dq, p, st, true);
   if (e != cudaSuccess) return e;
-  return go<gen_dkv_kernel<E, HD, T>>(p.plan.items, dkv, p, st);
+  return go<gen_dkv_kernel<E, HD, T>>(p.plan.items, dkv, p, st, true);
 }
 template <typename E, int T>
 cudaError_t run_hd(const SeqParams& p, bool back, cudaStream_t st) {
@@ -598,12 +608,10 @@ cudaError_t seq_reduce(const SeqParams& p, int dtype, cudaStream_t st) {
   const long long rows = d.gs > 1 ? p.S : (p.S < d.nst * d.T ? p.S : d.nst * d.T);
   const long long grid = ((long long)p.B * rows * p.K * (p.hd / 4) + 255) / 256;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  if (dtype == SWIN_DTYPE_BF16)
-    dkv_reduce_kernel<__nv_bfloat16><<<(unsigned)grid, 256, 0, st>>>(p);
-  else
-    dkv_reduce_kernel<float><<<(unsigned)grid, 256, 0, st>>>(p);
-  note_launch();
-  return cudaGetLastError();
+  const dim3 g((unsigned)grid);
+  return dtype == SWIN_DTYPE_BF16
+             ? launch_dependent(dkv_reduce_kernel<__nv_bfloat16>, g, 256, 0, st, p)
+             : launch_dependent(dkv_reduce_kernel<float>, g, 256, 0, st, p);
 }
 
 }  // namespace swin
