@@ -343,28 +343,48 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
         seq_wait(&sf[rb.s], rb.parity, abort, p.status);
         tc_fence_after();
         float v[KT];
-        tmem_load_cols<KT>(s_col, v);
-        tmem_wait_ld();
+        float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
         const bool plain =
             k0 + KT - 1 <= i0 && (i0 + kRows - 1 - k0 < p.window || k0 + KT <= p.sinks);
-        if (!plain) {
-          const int hi = i - k0, lo = hi - p.window + 1, sk = p.sinks - k0;
+        const int hi = i - k0, lo = hi - p.window + 1, sk = p.sinks - k0;
+        auto mask = [&](int c0) {
+          const uint32_t see = column_mask(lo - c0, hi - c0, sk - c0);
 #pragma unroll
-          for (int c0 = 0; c0 < KT; c0 += 32) {
-            const uint32_t see = column_mask(lo - c0, hi - c0, sk - c0);
+          for (int c = 0; c < 32; ++c)
+            if (!(see & (1u << c))) v[c0 + c] = -INFINITY;
+        };
+        auto top = [&](int c0) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!(see & (1u << c))) v[c0 + c] = -INFINITY;
+          for (int c = c0; c < c0 + 32; c += 8) {
+            m0 = fmaxf(fmaxf(m0, v[c]), v[c + 1]);
+            m1 = fmaxf(fmaxf(m1, v[c + 2]), v[c + 3]);
+            m2 = fmaxf(fmaxf(m2, v[c + 4]), v[c + 5]);
+            m3 = fmaxf(fmaxf(m3, v[c + 6]), v[c + 7]);
           }
+        };
+        // head_dim 128: the first half's maxima while the second half is on its way
+        // (440 us against 480 for 16384 tokens, 16 heads, window 4096); at 64 both
+        // halves at once (44 us against 46 for two sequences of 4096, window 512)
+        __syncwarp();
+        tmem_ld32(s_col, v);
+        if constexpr (HD > 64) {
+          tmem_wait_ld_regs(v);
+          tmem_ld32(s_col + 32, v + 32);
+          if (!plain) mask(0);
+          top(0);
+          tmem_wait_ld_regs(v + 32);
+          if (!plain) mask(32);
+        } else {
+          tmem_ld32(s_col + 32, v + 32);
+          tmem_wait_ld_regs(v);
+          reg_fence32(v + 32);
+          if (!plain) {
+            mask(0);
+            mask(32);
+          }
+          top(0);
         }
-        float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
-#pragma unroll
-        for (int c = 0; c < KT; c += 8) {
-          m0 = fmaxf(fmaxf(m0, v[c]), v[c + 1]);
-          m1 = fmaxf(fmaxf(m1, v[c + 2]), v[c + 3]);
-          m2 = fmaxf(fmaxf(m2, v[c + 4]), v[c + 5]);
-          m3 = fmaxf(fmaxf(m3, v[c + 6]), v[c + 7]);
-        }
+        top(32);
         const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * p.scale_log2;
         const bool move = mt > m + kSeqMove;
         const float f = move ? ex2(m - mt) : 1.f;   // 0 while m = -inf
