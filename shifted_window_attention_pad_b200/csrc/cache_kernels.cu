@@ -899,8 +899,7 @@ __device__ __forceinline__ void pick_bin(SelectShared& sh, uint32_t need) {
 // apart) in registers and one scan over the counts of every warp and round
 // gives all places (n <= 1024 R); R = 0 reads the weights again in every pass
 // and takes a contiguous run of positions per warp. Bound by the passes'
-// instructions: 36 us with the keys in shared memory for 64 x 32768 weights,
-// against the register form's figure in evict_long below.
+// instructions: 29 us for 64 x 32768 weights (36 with the keys in shared memory).
 template <int R>
 __global__ void __launch_bounds__(kSelThr)
     evict_select_kernel(const __grid_constant__ CacheParams p, int* kept) {

@@ -96,6 +96,10 @@ size_t span(long long tokens, long long stride, int heads, int hd, int dtype) {
   return (size_t)((tokens - 1) * stride + (long long)heads * hd) * elem_bytes(dtype);
 }
 
+size_t cache_bytes(const CacheParams& p, int dtype) {
+  return (size_t)p.pages * p.K * p.ps * p.hd * elem_bytes(dtype);
+}
+
 int check_cache(const swin_kvcache_desc* d) {
   if (!d) return SWIN_ERR_INVALID_ARG;
   const int rc = check_heads(d->heads, d->kv_heads, d->head_dim, d->dtype);
@@ -109,6 +113,8 @@ int check_cache(const swin_kvcache_desc* d) {
   const long long len = (long long)d->max_pages * d->page_size;
   if (len > 0x7fffffffLL || len * d->B > (1LL << 40) / d->kv_heads) return SWIN_ERR_INVALID_ARG;
   if (d->heads / d->kv_heads > 1024 || (long long)d->B * d->heads > 0x7fffffffLL)
+    return SWIN_ERR_INVALID_ARG;
+  if ((double)d->num_pages * d->kv_heads * d->page_size * d->head_dim > (double)(1LL << 48))
     return SWIN_ERR_INVALID_ARG;
   // evict's own fields are checked by that call; here only that they can size a workspace
   if (d->budget < 0 || d->budget > len || d->recent < 0) return SWIN_ERR_INVALID_ARG;
@@ -166,7 +172,8 @@ int swin_seqattn_fwd(const swin_seqattn_desc* desc, const void* q, const void* k
   const size_t nk = span(tok, p.ks, p.K, p.hd, desc->dtype);
   const size_t no = (size_t)tok * p.H * p.hd * elem_bytes(desc->dtype);
   if (overlap(out, no, q, nq) || overlap(out, no, k, nk) || overlap(out, no, v, nk) ||
-      overlap(lse, (size_t)tok * p.H * 4, out, no))
+      overlap(lse, (size_t)tok * p.H * 4, q, nq) || overlap(lse, (size_t)tok * p.H * 4, k, nk) ||
+      overlap(lse, (size_t)tok * p.H * 4, v, nk) || overlap(lse, (size_t)tok * p.H * 4, out, no))
     return SWIN_ERR_INVALID_ARG;
   rc = check_ws(workspace, workspace_bytes, seq_workspace(p));
   if (rc) return rc;
@@ -188,15 +195,20 @@ int swin_seqattn_bwd(const swin_seqattn_desc* desc, const void* q, const void* k
     if (!al16(x)) return SWIN_ERR_INVALID_ARG;
   if (lengths && !al4(lengths)) return SWIN_ERR_INVALID_ARG;
   SeqParams p = seq_params(desc);
-  const size_t no = (size_t)p.B * p.S * p.H * p.hd * elem_bytes(desc->dtype);
-  // dq, dk, dv may interleave in one buffer, never with out or dout, and each
+  const long long tok = (long long)p.B * p.S;
+  const size_t no = (size_t)tok * p.H * p.hd * elem_bytes(desc->dtype);
+  const size_t nq = span(tok, p.qs, p.H, p.hd, desc->dtype);
+  const size_t nk = span(tok, p.ks, p.K, p.hd, desc->dtype);
+  // dq, dk, dv may interleave in one buffer, never with out, lse or dout, and each
   // starts where nothing else does
-  if (dq == dk || dq == dv || dk == dv || dq == q || dk == k || dv == v ||
-      overlap(dq, span((long long)p.B * p.S, p.qs, p.H, p.hd, desc->dtype), out, no) ||
-      overlap(dq, span((long long)p.B * p.S, p.qs, p.H, p.hd, desc->dtype), dout, no) ||
-      overlap(dk, span((long long)p.B * p.S, p.ks, p.K, p.hd, desc->dtype), dout, no) ||
-      overlap(dv, span((long long)p.B * p.S, p.ks, p.K, p.hd, desc->dtype), dout, no))
+  if (dq == dk || dq == dv || dk == dv || dq == q || dk == k || dv == v)
     return SWIN_ERR_INVALID_ARG;
+  const void* grads[] = {dq, dk, dv};
+  for (const void* x : grads) {
+    const size_t n = x == dq ? nq : nk;
+    if (overlap(x, n, out, no) || overlap(x, n, dout, no) || overlap(x, n, lse, (size_t)tok * p.H * 4))
+      return SWIN_ERR_INVALID_ARG;
+  }
   rc = check_ws(workspace, workspace_bytes, seq_workspace(p));
   if (rc) return rc;
   seq_carve(p, workspace);
@@ -225,11 +237,16 @@ int swin_kvcache_append(const swin_kvcache_desc* desc, int32_t T, const void* k,
   int rc = check_cache(desc);
   if (rc) return rc;
   if (T < 1 || !al16(k) || !al16(v) || !al4(lengths) || !al4(page_table) || !al16(k_cache) ||
-      !al16(v_cache) || (counts && !al4(counts)) || k_cache == v_cache)
+      !al16(v_cache) || (counts && !al4(counts)))
     return SWIN_ERR_INVALID_ARG;
   rc = check_ws(workspace, workspace_bytes, kWsHeader);
   if (rc) return rc;
   CacheParams p = cache_params(desc);
+  const size_t nc = cache_bytes(p, desc->dtype);
+  const size_t nn = span((long long)p.B * T, p.ks, p.K, p.hd, desc->dtype);
+  if (overlap(k_cache, nc, v_cache, nc) || overlap(k, nn, k_cache, nc) ||
+      overlap(k, nn, v_cache, nc) || overlap(v, nn, k_cache, nc) || overlap(v, nn, v_cache, nc))
+    return SWIN_ERR_INVALID_ARG;
   if ((long long)T * p.K * p.hd > (1LL << 31) || (long long)T * p.B * p.K * p.hd > (1LL << 38))
     return SWIN_ERR_INVALID_ARG;
   p.status = (int*)workspace;
@@ -246,7 +263,7 @@ int swin_kvcache_decode(const swin_kvcache_desc* desc, const void* q, const void
   int rc = check_cache(desc);
   if (rc) return rc;
   if (!al16(q) || !al4(lengths) || !al4(page_table) || !al16(k_cache) || !al16(v_cache) ||
-      !al16(out) || (lse && !al16(lse)) || k_cache == v_cache)
+      !al16(out) || (lse && !al16(lse)))
     return SWIN_ERR_INVALID_ARG;
   if ((k_new == nullptr) != (v_new == nullptr)) return SWIN_ERR_INVALID_ARG;
   if (k_new && (!al16(k_new) || !al16(v_new))) return SWIN_ERR_INVALID_ARG;
@@ -254,6 +271,16 @@ int swin_kvcache_decode(const swin_kvcache_desc* desc, const void* q, const void
   if (weights && (!al16(weights) || !al16(new_weights) || !(desc->flags & SWIN_FLAG_KV_WEIGHTS)))
     return SWIN_ERR_INVALID_ARG;
   CacheParams p = cache_params(desc);
+  // out is written while other blocks still read q and the new rows
+  const size_t nc = cache_bytes(p, desc->dtype), nw = (size_t)p.B * p.K * p.max_len * 4;
+  const size_t no = (size_t)p.B * p.H * p.hd * elem_bytes(desc->dtype);
+  const size_t nn = span(p.B, p.ks, p.K, p.hd, desc->dtype);
+  if (overlap(k_cache, nc, v_cache, nc) ||
+      overlap(out, no, q, span(p.B, p.qs, p.H, p.hd, desc->dtype)) || overlap(out, no, k_new, nn) ||
+      overlap(out, no, v_new, nn) || overlap(out, no, k_cache, nc) || overlap(out, no, v_cache, nc) ||
+      overlap(lse, (size_t)p.B * p.H * 4, out, no) ||
+      (weights != new_weights && overlap(weights, nw, new_weights, nw)))
+    return SWIN_ERR_INVALID_ARG;
   rc = check_ws(workspace, workspace_bytes, kWsHeader + cache_workspace(p, desc->dtype));
   if (rc) return rc;
   p.status = (int*)workspace;
@@ -274,11 +301,11 @@ int swin_kvcache_evict(const swin_kvcache_desc* desc, const float* weights,
     return SWIN_ERR_INVALID_ARG;
   if (!al16(weights) || !al16(new_weights) || !al4(lengths) || !al4(new_lengths) ||
       !al4(page_table) || !al4(dst_page_table) || !al16(k_cache) || !al16(v_cache) ||
-      (kept && !al4(kept)) || k_cache == v_cache)
+      (kept && !al4(kept)))
     return SWIN_ERR_INVALID_ARG;
   CacheParams p = cache_params(desc);
-  const size_t nw = (size_t)p.B * p.K * p.max_len * 4;
-  if (overlap(weights, nw, new_weights, nw) || overlap(lengths, p.B * 4, new_lengths, p.B * 4) ||
+  const size_t nw = (size_t)p.B * p.K * p.max_len * 4, nc = cache_bytes(p, desc->dtype);
+  if (overlap(k_cache, nc, v_cache, nc) || overlap(weights, nw, new_weights, nw) || overlap(lengths, p.B * 4, new_lengths, p.B * 4) ||
       page_table == dst_page_table)
     return SWIN_ERR_INVALID_ARG;
   rc = check_ws(workspace, workspace_bytes, kWsHeader + cache_workspace(p, desc->dtype));

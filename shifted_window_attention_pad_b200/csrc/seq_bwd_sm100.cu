@@ -9,14 +9,14 @@
 //    dP^T = V dO^T over the queries in steps of 64 (thread = key), dV += P^T dO,
 //    dK += dS^T Q.
 // One kernel template runs both: a stationary pair of 128-row tiles (Q, dO or
-// K, V), a streamed pair of 64-row tiles, two TMEM buffers of S | dP (64 + 64
-// columns) and the accumulators. P and dS are rounded to bf16 over their own
+// K, V), a streamed pair of 64-row tiles, two or three TMEM buffers of S | dP
+// (64 + 64 columns) and the accumulators. P and dS are rounded to bf16 over their own
 // columns and are the A operand of the gradient products from TMEM (off by
 // 2^-8 of each term at most); sums are fp32 in TMEM.
 //
 // D_i = dO_i.o_i uses the stored, rounded o. Where a row sees few keys its dS is
 // a small difference of dP and D and that rounding would show, so items of at
-// at most kFewKeys keys take D = sum_j P_ij dP_ij from a pass of their own
+// most kFewKeys keys take D = sum_j P_ij dP_ij from a pass of their own
 // first (and leave it for the key side): an error of 0.11 of the gradients' RMS
 // in the first rows of a sequence becomes that of other rows. Longer rows would
 // pay two more products per step for an error already below the outputs' own
@@ -24,10 +24,14 @@
 //
 // Warps: a softmax warpgroup per TMEM buffer, taking the steps in turn (thread =
 // row); then the TMA producer, a warp that issues S and dP and owns TMEM, and one
-// that issues the gradient products. Bound: the tensor pipe at head_dim 128 (per 128 x 64 step S
-// and dP with N = 64, which read both operands from shared memory at 1.5 times
-// the cost of N = 128, and one or two gradient products), the exp unit and the
-// softmax warps' issue slots at 64.
+// that issues the gradient products. Bound: the tensor pipe at head_dim 128 (per
+// 128 x 64 step S and dP with N = 64, which read both operands from shared memory
+// at 1.5 times the cost of N = 128, and one or two gradient products), the exp
+// unit and the softmax warps' latencies at 64. Measured: 8192 causal tokens, 8
+// heads x 128 (2 key heads), 476 us for the whole backward, 208 us of them the
+// query side (tensor pipe active 52% of the time, 65% with what N = 64 loses) and
+// 298 us the key side (47%) when profiled; two ragged sequences of 4096, 16 heads
+// x 64, window 512: 135 us (58 and 73 when profiled).
 #include "seq_tc.cuh"
 
 namespace swin {
@@ -504,8 +508,9 @@ __global__ void __launch_bounds__(BwdTmem<HD, KEYS>::kThreads, 1)
         const float4* dv = lv + kStep / 4;
         const float sub = sums ? 0.f : nd;
         const bool few = KEYS ? it.few(p, c0) : total > steps;
-        // a half of the step's columns at a time (two halves in registers at once, with
-        // two warpgroups of twice the registers: 150 us against the figure above)
+        // a half of the step's columns at a time (both halves in registers at once needs
+        // two warpgroups of twice the registers: 150 us against 146 for the window 512
+        // case above when it was tried)
 #pragma unroll
         for (int h = 0; h < kStep; h += 32) {
           float v[32], g[32];

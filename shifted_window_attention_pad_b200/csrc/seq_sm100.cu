@@ -16,9 +16,9 @@
 //
 // TMEM: per query tile a ring of NB S buffers of KT keys, and O. With two or three
 // buffers the next S is there when a softmax step ends; steps of 64 keys make
-// room for them (a single 128-key buffer: 0.579 ms against 0.505 for 16384
-// tokens, 16 heads x 128, window 4096; 61 us against 49 for two ragged 4096-token
-// sequences, 16 heads x 64, window 512).
+// room for them (a single 128-key buffer: 579 us against 505, at the time, for
+// 16384 tokens, 16 heads x 128, window 4096; 61 us against 49 for two ragged
+// 4096-token sequences, 16 heads x 64, window 512).
 //
 // Warps: 0-3 and 4-7 one softmax warpgroup per query tile (thread = row), 8
 // the TMA producer, 9 issues S and owns TMEM, 10 issues O += P V. Keys and
@@ -26,7 +26,16 @@
 //
 // Bound: per 128 x 128 tile of a head the tensor pipe needs 8 hd cycles (S and
 // O at 8192 FLOP per cycle and SM) and the exp unit 1024 (16 per cycle), so
-// head_dim 128 is bound by both alike, head_dim 64 by the exp unit.
+// head_dim 128 is bound by both alike, head_dim 64 by the exp unit. Measured: 437 us
+// for the first case above (1100 TFLOP/s), 44 us for the second. The tensor pipe is
+// then busy for two thirds of the time, counting the half more that S with N = 64
+// costs (both operands come from shared memory), the exp unit for half: a step
+// goes through two products, the softmax and four barriers, each waiting for the
+// one before, and TMEM has no room for more steps in flight. On the exp unit's
+// side there is nothing to gain: a polynomial on the FMA pipe for a quarter to all
+// of the exponentials, or two threads per row, left the time as it was; one warp
+// that issues all products took 759 us, four (one for each product of a query
+// tile) 470.
 #include "seq_tc.cuh"
 
 namespace swin {

@@ -200,6 +200,41 @@ def test_cache_calls_refuse_bad_arguments(L):
     assert L.swin_kvcache_evict(d, *ev, P((1 << 20) + 128), BIG, None) == -3
 
 
+def test_outputs_that_overlap_inputs_are_refused(L):
+    d, c = ctypes.byref(_seq()), ctypes.byref(_cache())
+    behind = lambda n: P((1 << 20) + (n << 28) + 256)   # inside what AT(n) holds
+    # q k v out lse: lse on each of the others
+    for x in range(4):
+        assert L.swin_seqattn_fwd(d, AT(0), AT(1), AT(2), None, AT(3), behind(x), GOOD, BIG,
+                                  None) == -1, x
+    # q k v out lse dout dq dk dv: a gradient inside out, lse or dout
+    for x in (6, 7, 8):
+        for y in (3, 4, 5):
+            a = [AT(z) for z in range(9)]
+            a[x] = behind(y)
+            assert L.swin_seqattn_bwd(d, *a[:3], None, *a[3:], GOOD, BIG, None) == -1, (x, y)
+    # k v counts lengths table kc vc: one cache inside the other, tokens inside a cache
+    for x, y in ((6, 5), (0, 5), (0, 6), (1, 5), (1, 6)):
+        a = [AT(0), AT(1), None] + [AT(z) for z in range(3, 7)]
+        a[x] = behind(y)
+        assert L.swin_kvcache_append(c, 1, *a, GOOD, BIG, None) == -1, (x, y)
+    # q k_new v_new lengths table kc vc weights new_weights out lse
+    for x, y in ((6, 5), (9, 0), (9, 1), (9, 2), (9, 5), (9, 6), (10, 9), (8, 7)):
+        a = [AT(z) for z in range(11)]
+        a[x] = behind(y)
+        assert L.swin_kvcache_decode(c, *a, GOOD, BIG, None) == -1, (x, y)
+    # weights lengths table dst kc vc new_weights new_lengths kept
+    a = [AT(z) for z in range(8)] + [None]
+    a[5] = behind(4)
+    assert L.swin_kvcache_evict(c, *a, GOOD, BIG, None) == -1
+
+
+def test_caches_past_what_is_addressed_are_refused():
+    with pytest.raises(sb.SwinWattnError):
+        sb.swin_kvcache_workspace_size(_cache(num_pages=0x7fffffff, page_size=65536, max_pages=1,
+                                              head_dim=256))
+
+
 def test_wrappers_refuse_host_tensors():
     d = sb.make_seq_desc(1, 4, 2, 64, 0, "bf16")
     x = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
