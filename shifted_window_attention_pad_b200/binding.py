@@ -7,6 +7,7 @@ stream, and turns negative status codes into exceptions. torch is used for
 device memory and streams only. There is no fallback: if the library is
 missing, the first call raises.
 """
+import contextlib
 import ctypes
 import os
 
@@ -484,10 +485,13 @@ def swin_kvcache_workspace_size(desc):
     return _workspace_size("swin_kvcache_workspace_size", desc)
 
 
-def _new_ws(size, device):
-    """Only the header (the device status word) has to start as zeros."""
-    ws = torch.empty(size, dtype=torch.uint8, device=device)
-    ws[:256].zero_()
+def _new_ws(size, device, stream=None):
+    """Only the header (the device status word) has to start as zeros. With a
+    stream: allocated and zeroed on it, so that the memory is not handed on
+    while the stream still works in it."""
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+        ws = torch.empty(size, dtype=torch.uint8, device=device)
+        ws[:256].zero_()
     return ws
 
 
@@ -515,7 +519,7 @@ def swin_seqattn_fwd(desc, q, k, v, lengths, out, lse=None, workspace=None, stre
             _maybe(lengths, "lengths", torch.int32, (desc.B,), dev),
             _dense(out, "out", el, sq, dev), _maybe(lse, "lse", torch.float32, sl, dev))
     if workspace is None:
-        workspace = new_seq_workspace(desc, q.device)
+        workspace = _new_ws(swin_seqattn_workspace_size(desc), q.device, stream)
     _run("swin_seqattn_fwd", lib().swin_seqattn_fwd, dev, workspace, stream, desc, *args)
     return out
 
@@ -532,7 +536,7 @@ def swin_seqattn_bwd(desc, q, k, v, lengths, out, lse, dout, dq, dk, dv, workspa
             _dense(dout, "dout", el, sq, dev), _tokens(dq, "dq", el, sq, qs, dev),
             _tokens(dk, "dk", el, sk, ks, dev), _tokens(dv, "dv", el, sk, ks, dev))
     if workspace is None:
-        workspace = new_seq_workspace(desc, q.device)
+        workspace = _new_ws(swin_seqattn_workspace_size(desc), q.device, stream)
     _run("swin_seqattn_bwd", lib().swin_seqattn_bwd, dev, workspace, stream, desc, *args)
     return dq, dk, dv
 
@@ -587,7 +591,7 @@ def swin_kvcache_append(desc, k, v, counts, lengths, page_table, k_cache, v_cach
             _maybe(counts, "counts", torch.int32, (d.B,), dev),
             *_cache_args(d, el, dev, lengths, page_table, k_cache, v_cache))
     if workspace is None:
-        workspace = _new_ws(256, k.device)
+        workspace = _new_ws(256, k.device, stream)
     _run("swin_kvcache_append", lib().swin_kvcache_append, dev, workspace, stream, d, *args)
 
 
@@ -605,7 +609,7 @@ def swin_kvcache_decode(desc, q, k_new, v_new, lengths, page_table, k_cache, v_c
             _maybe(new_weights, "new_weights", torch.float32, sw, dev),
             _dense(out, "out", el, so, dev), _maybe(lse, "lse", torch.float32, (B, H), dev))
     if workspace is None:
-        workspace = new_cache_workspace(d, q.device)
+        workspace = _new_ws(swin_kvcache_workspace_size(d), q.device, stream)
     _run("swin_kvcache_decode", lib().swin_kvcache_decode, dev, workspace, stream, d, *args)
     return out
 
@@ -621,7 +625,7 @@ def swin_kvcache_evict(desc, weights, lengths, page_table, dst_page_table, k_cac
             _dense(new_lengths, "new_lengths", torch.int32, (d.B,), dev),
             _maybe(kept, "kept", torch.int32, (d.B, d.kv_heads, d.budget), dev))
     if workspace is None:
-        workspace = new_cache_workspace(d, weights.device)
+        workspace = _new_ws(swin_kvcache_workspace_size(d), weights.device, stream)
     _run("swin_kvcache_evict", lib().swin_kvcache_evict, dev, workspace, stream, d, *args)
     return new_weights, new_lengths
 

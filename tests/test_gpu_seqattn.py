@@ -235,6 +235,32 @@ def test_two_streams_with_a_workspace_each():
             assert torch.equal(x, one[name]), name
 
 
+def test_own_workspaces_belong_to_the_stream(monkeypatch):
+    """A call with a stream and no workspace takes its workspace on that stream:
+    on the current one its memory could be handed on while the call runs."""
+    q, k, v, g = make(1, 300, 4, 2, 64, "bf16", seed=29)
+    one = run(q, k, v, g, 100, 2)
+    d = sb.seq_desc_for(q, k, window=100, sinks=2)
+    s, on = torch.cuda.Stream(), []
+    empty = torch.empty
+
+    def recorded(*a, **kw):
+        on.append(torch.cuda.current_stream().cuda_stream)
+        return empty(*a, **kw)
+
+    out, lse = torch.empty_like(q), torch.empty_like(one["lse"])
+    grads = [torch.empty_like(t) for t in (q, k, v)]
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch, "empty", recorded)
+    sb.swin_seqattn_fwd(d, q, k, v, None, out, lse, stream=s)
+    sb.swin_seqattn_bwd(d, q, k, v, None, out, lse, g, *grads, stream=s)
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert on == [s.cuda_stream] * 2
+    for x, name in zip((out, lse, *grads), ALL):
+        assert torch.equal(x, one[name]), name
+
+
 def test_timeouts_are_reported():
     """The kernels' bounded wait: a barrier that nothing arrives on ends the call
     with a status, and the workspace serves the next call."""
