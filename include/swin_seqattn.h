@@ -102,9 +102,8 @@ int swin_seqattn_bwd(const swin_seqattn_desc* desc, const void* q, const void* k
  * head_dim as above; window, sinks >= 0. q_stride and kv_stride: elements from
  * one token to the next in q (decode) and in the new keys and values (decode,
  * append); 0 = contiguous. At most 1024 query heads to a kv head;
- * B * kv_heads * max_pages * page_size < 2^40,
- * max_pages * page_size < 2^31 and num_pages * kv_heads * page_size * head_dim
- * at most 2^48. Outputs must not overlap inputs or one another, except where
+ * B * kv_heads * max_pages * page_size at most 2^40, max_pages * page_size at
+ * most 2^30 and num_pages * kv_heads * page_size * head_dim at most 2^48. Outputs must not overlap inputs or one another, except where
  * a call says so. */
 enum swin_kvcache_flags {
   SWIN_FLAG_KV_WEIGHTS = 1 << 8 /* decode calls will accumulate weights: the workspace also

@@ -111,7 +111,7 @@ int check_cache(const swin_kvcache_desc* d) {
       bad_stride(d->kv_stride, d->kv_heads, d->head_dim, d->dtype))
     return SWIN_ERR_INVALID_ARG;
   const long long len = (long long)d->max_pages * d->page_size;
-  if (len > 0x7fffffffLL || len * d->B > (1LL << 40) / d->kv_heads) return SWIN_ERR_INVALID_ARG;
+  if (len > (1LL << 30) || len * d->B > (1LL << 40) / d->kv_heads) return SWIN_ERR_INVALID_ARG;
   if (d->heads / d->kv_heads > 1024 || (long long)d->B * d->heads > 0x7fffffffLL)
     return SWIN_ERR_INVALID_ARG;
   if ((double)d->num_pages * d->kv_heads * d->page_size * d->head_dim > (double)(1LL << 48))

@@ -230,6 +230,11 @@ def test_outputs_that_overlap_inputs_are_refused(L):
 
 
 def test_caches_past_what_is_addressed_are_refused():
+    """Positions are counted in 32 bits, with room for a tile behind the last."""
+    long = dict(page_size=65536, max_pages=1 << 14, num_pages=1 << 15)
+    assert sb.swin_kvcache_workspace_size(_cache(**long)) > 0
+    with pytest.raises(sb.SwinWattnError):
+        sb.swin_kvcache_workspace_size(_cache(**dict(long, max_pages=(1 << 14) + 1)))
     with pytest.raises(sb.SwinWattnError):
         sb.swin_kvcache_workspace_size(_cache(num_pages=0x7fffffff, page_size=65536, max_pages=1,
                                               head_dim=256))
