@@ -536,10 +536,11 @@ cudaError_t run_tile(const SeqParams& p, bool back, cudaStream_t st) {
 }  // namespace
 
 // 64 x 64 tiles feed the FMA pipe better, 32 x 32 tiles give four times the blocks;
-// the small ones are for work that would leave SMs without a block (and for heads
-// above 128, whose tiles would not fit shared memory).
+// the small ones are for work that would leave SMs without a block, for sequences
+// that one of them holds (and for heads above 128, whose large tiles would not fit
+// shared memory).
 int seq_generic_tile(int B, int S, int H, int hd) {
-  return hd > 128 || (long long)B * H * ((S + 63) / 64) < kSeqSms ? 32 : 64;
+  return hd > 128 || S <= 32 || (long long)B * H * ((S + 63) / 64) < kSeqSms ? 32 : 64;
 }
 
 DkvPlan make_dkv_plan(int B, int S, int K, int G, int hd, int window, int sinks, int T) {
