@@ -842,31 +842,65 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int kSelThr = 1024, kSelRegs = 32;   // positions held in registers: 32 x 1024
+constexpr int kSelThr = 1024, kSelRound = 4 * kSelThr;   // four positions a thread and round
 
-__device__ __forceinline__ uint32_t load_once(const float* p) {
-  uint32_t v;
-  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
+// Weights of positions x .. x + 3 (zeros at and beyond n), in one load if rows start
+// on 16 bytes.
+__device__ __forceinline__ void load_weights(const float* w, int x, int n, bool wide,
+                                             uint32_t (&v)[4]) {
+  v[0] = v[1] = v[2] = v[3] = 0u;
+  if (wide && x + 3 < n) {
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "l"(w + x));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (x + e < n) asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v[e]) : "l"(w + x + e));
+  }
 }
 
 struct SelectShared {
-  uint32_t hist[4 * 2048];   // four copies; then counts in position order
-  uint32_t bin, need, warp_sum[32];
+  alignas(16) uint32_t hist[2048 * 4];   // four counts of each bin; then of each round and warp
+  uint32_t sums[3][1024];                // a cluster: this block's counts of two bins, by pass
+  uint32_t bin, need, total, warp_sum[32];
 };
 
-// One digit of the threshold from the block's histograms (2048 bins, two a
-// thread, from the top): the bin that holds the need-th largest key and how many
-// of it are needed.
-__device__ __forceinline__ void pick_bin(SelectShared& sh, uint32_t need) {
+// The blocks of a cluster: all have come here, and see what each wrote to its shared
+// memory; a word of block `rank`.
+__device__ __forceinline__ void team_sync() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t team_read(const uint32_t* at, int rank) {
+  uint32_t a, v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_u32(at)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// One digit of the threshold from the histograms (2048 bins, two a thread, from the
+// top): the bin that holds the need-th largest key and how many of it are needed.
+// The same in every block of a cluster.
+template <int C>
+__device__ __forceinline__ void pick_bin(SelectShared& sh, int pass, uint32_t need) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, top = 2047 - 2 * threadIdx.x;
   __syncthreads();
-  uint32_t c0 = 0, c1 = 0;   // bins top, top - 1
+  const uint4 h = *reinterpret_cast<const uint4*>(&sh.hist[top * 4]);
+  const uint4 g = *reinterpret_cast<const uint4*>(&sh.hist[top * 4 - 4]);
+  uint32_t c0 = (h.x + h.y) + (h.z + h.w), c1 = (g.x + g.y) + (g.z + g.w);   // bins top, top - 1
+  if constexpr (C > 1) {   // at most 32768 each
+    sh.sums[pass][threadIdx.x] = c0 | c1 << 16;
+    team_sync();
+    uint32_t t[C];
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const uint2 h = *reinterpret_cast<const uint2*>(&sh.hist[v * 2048 + top - 1]);
-    c0 += h.y;
-    c1 += h.x;
+    for (int v = 0; v < C; ++v) t[v] = team_read(&sh.sums[pass][threadIdx.x], v);
+    c0 = c1 = 0;
+#pragma unroll
+    for (int v = 0; v < C; ++v) {
+      c0 += t[v] & 0xffffu;
+      c1 += t[v] >> 16;
+    }
   }
   const uint32_t sum = c0 + c1;
   uint32_t inc = sum;
@@ -889,106 +923,132 @@ __device__ __forceinline__ void pick_bin(SelectShared& sh, uint32_t need) {
   __syncthreads();
 }
 
-// Which positions of (b, kv head) stay: one block each. The always-kept positions
-// have the largest key, so what stays is the `budget` largest keys of the
+// Which positions of (b, kv head) stay: a cluster of C blocks each. The always-kept
+// positions have the largest key, so what stays is the `budget` largest keys of the
 // sequence, ties at the threshold in order of position. The threshold is found
 // digit by digit (11, 11 and 10 bits; wide digits, since weights share few
 // exponents and shared-memory atomics on one bin queue up). A kept
 // position's place in the output is the number of larger keys before it plus
-// the ties before it that stay. With R > 0 a thread holds its R positions (1024
-// apart) in registers and one scan over the counts of every warp and round
-// gives all places (n <= 1024 R); R = 0 reads the weights again in every pass
-// and takes a contiguous run of positions per warp. Bound by the passes'
-// instructions: 29 us for 64 x 32768 weights (36 with the keys in shared memory).
-template <int R>
-__global__ void __launch_bounds__(kSelThr)
+// the ties before it that stay. With R > 0 a thread holds R groups of four
+// positions (4096 apart) in registers and one scan over the counts of every warp
+// and round gives all places (n <= 4096 R C); R = 0 (one block) reads the weights
+// again in every pass and takes a contiguous run of positions per warp. Bound by
+// the passes' instructions: 25 us for 64 x 32768 weights (29 with a position a
+// thread at a time and the loads that takes).
+template <int R, int C>
+__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kSelThr)
     evict_select_kernel(const __grid_constant__ CacheParams p, int* kept) {
-  __shared__ __align__(16) SelectShared sh;
+  static_assert(C == 1 || R > 0, "a cluster holds its positions in registers");
+  __shared__ SelectShared sh;
   ptx::grid_dep_launch();
-  const int b = blockIdx.x / p.K, kh = blockIdx.x - b * p.K;
+  const int bk = blockIdx.x / C, rank = blockIdx.x - bk * C, b = bk / p.K, kh = bk - b * p.K;
   const int n = cache_len(p, b), keep = min(n, p.budget);
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const float* w = p.w + ((long long)b * p.K + kh) * p.max_len;
-  float* w_out = p.w_out + ((long long)b * p.K + kh) * p.max_len;
-  int* out = kept + ((long long)b * p.K + kh) * p.budget;
-  if (kh == 0 && threadIdx.x == 0) p.new_len[b] = keep;
-  const int lo = p.sinks, hi = n - p.recent;       // positions outside stay
-  auto key_of = [&](int x) {
-    return x >= n ? 0u : (x < lo || x >= hi ? 0xffffffffu : weight_key(w[x]));
-  };
-  uint32_t keys[R > 0 ? R : 1];   // weights as they come, then keys
-  const int rounds = R > 0 ? min(R, (n + kSelThr - 1) / kSelThr) : (n + kSelThr - 1) / kSelThr;
-  if constexpr (R > 0) {
-    // all loads first, in flight together (left to itself the compiler waits for each)
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      keys[r] = 0u;
-      if (r < rounds)
-        keys[r] = load_once(w + min(r * kSelThr + (int)threadIdx.x, max(n - 1, 0)));
-    }
-    asm volatile("" ::: "memory");
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int x = r * kSelThr + threadIdx.x;
-      const uint32_t k = weight_key(__uint_as_float(keys[r]));
-      keys[r] = x >= n ? 0u : (x < lo || x >= hi ? 0xffffffffu : k);
-    }
-  }
-  for (int x = keep + threadIdx.x; x < p.budget; x += kSelThr) out[x] = -1;
-  for (long long x = keep + threadIdx.x; x < p.max_len; x += kSelThr) w_out[x] = 0.f;
-  if (n <= p.budget) {
-    for (int x = threadIdx.x; x < n; x += kSelThr) {
+  const float* w = p.w + (long long)bk * p.max_len;
+  float* w_out = p.w_out + (long long)bk * p.max_len;
+  int* out = kept + (long long)bk * p.budget;
+  if (kh == 0 && rank == 0 && threadIdx.x == 0) p.new_len[b] = keep;
+  const int me = rank * kSelThr + threadIdx.x;
+  if (n <= p.budget) {   // (every block of the cluster)
+    for (int x = me; x < n; x += C * kSelThr) {
       out[x] = x;
       w_out[x] = w[x];
     }
+    for (int x = n + me; x < p.budget; x += C * kSelThr) out[x] = -1;
+    for (int x = n + me; x < p.max_len; x += C * kSelThr) w_out[x] = 0.f;
     return;
   }
+  const int lo = p.sinks, hi = n - p.recent;       // positions outside stay
+  const bool wide = (p.max_len & 3) == 0;
+  auto key_of = [&](int x, uint32_t raw) {
+    return x >= n ? 0u : (x < lo || x >= hi ? 0xffffffffu : weight_key(__uint_as_float(raw)));
+  };
+  // rounds of a block, and this thread's first position
+  const int rounds = ((n + C - 1) / C + kSelRound - 1) / kSelRound;
+  const int x0 = rank * rounds * kSelRound + 4 * threadIdx.x;
+  uint32_t keys[R > 0 ? R : 1][4];   // weights as they come, then keys
+  if constexpr (R > 0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) load_weights(w, x0 + r * kSelRound, r < rounds ? n : 0, wide, keys[r]);
+    asm volatile("" ::: "memory");   // all loads before the first use of one
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        keys[r][e] = r < rounds ? key_of(x0 + r * kSelRound + e, keys[r][e]) : 0u;
+  }
+  for (int x = keep + me; x < p.max_len; x += C * kSelThr) w_out[x] = 0.f;
   uint32_t prefix = 0, need = (uint32_t)p.budget;
-#pragma unroll 1
+#pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
-    const int bits = pass == 0 ? 21 : (pass == 1 ? 10 : 0);       // below the digit
-    const int above = pass == 0 ? 0 : (pass == 1 ? 21 : 10);      // 0: every key counts
-    const uint32_t digit = pass == 2 ? 1023u : 2047u;
+    constexpr int kShift[3] = {21, 10, 0};
     uint4* z = reinterpret_cast<uint4*>(sh.hist);
     z[threadIdx.x] = z[kSelThr + threadIdx.x] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    uint32_t* mine = sh.hist + (warp & 3) * 2048;
+    uint32_t* mine = sh.hist + (lane & 3);   // lanes of a warp that share a bin queue up
+    // keys that start with the digits so far: from `first`, this many of them
+    const uint32_t first = pass == 0 ? 1u : prefix << (pass == 1 ? 21 : 10);
+    const uint32_t many = pass == 0 ? 0xffffffffu : (pass == 1 ? 1u << 21 : 1u << 10);
     auto count = [&](uint32_t k) {
-      if (k != 0 && (pass == 0 || (k >> above) == prefix))
-        atomicAdd(&mine[(k >> bits) & digit], 1u);
+      if (k - first < many) atomicAdd(&mine[(k >> kShift[pass] & (pass == 2 ? 1023u : 2047u)) * 4], 1u);
     };
     if constexpr (R > 0) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (r >= rounds) break;
-        count(keys[r]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) count(keys[r][e]);
       }
     } else {
-      for (int r = 0; r < rounds; ++r) count(key_of(r * kSelThr + threadIdx.x));
+      for (int x = 4 * threadIdx.x; x < n; x += kSelRound) {
+        uint32_t v[4];
+        load_weights(w, x, n, wide, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) count(key_of(x + e, v[e]));
+      }
     }
-    pick_bin(sh, need);
+    pick_bin<C>(sh, pass, need);
     prefix = pass == 0 ? sh.bin : (prefix << (pass == 1 ? 11 : 10)) | sh.bin;
     need = sh.need;
     __syncthreads();
   }
   const uint32_t thr = prefix, lt = (1u << lane) - 1u;
-  auto emit = [&](int x, uint32_t k, uint32_t gt_before, uint32_t eq_before, float weight) {
-    const uint32_t gt = __ballot_sync(0xffffffffu, k > thr);
-    const uint32_t eq = __ballot_sync(0xffffffffu, k == thr);
-    const uint32_t tie = eq_before + __popc(eq & lt);
-    if (k > thr || (k == thr && tie < need)) {
-      const uint32_t at = gt_before + __popc(gt & lt) + min(tie, need);
-      out[at] = x;
-      w_out[at] = weight;
+  // Four positions of a thread from x on, behind gt larger keys and eq ties.
+  auto emit = [&](int x, const uint32_t (&k)[4], const uint32_t (&weight)[4], uint32_t gt,
+                  uint32_t eq) {
+    uint32_t g[4], q[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      g[e] = __ballot_sync(0xffffffffu, k[e] > thr);
+      q[e] = __ballot_sync(0xffffffffu, k[e] == thr);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      gt += __popc(g[e] & lt);
+      eq += __popc(q[e] & lt);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool larger = k[e] > thr, tie = k[e] == thr;
+      if (larger || (tie && eq < need)) {
+        const uint32_t at = gt + min(eq, need);
+        out[at] = x + e;
+        w_out[at] = __uint_as_float(weight[e]);
+      }
+      gt += larger;
+      eq += tie;
     }
   };
   if constexpr (R > 0) {
     // larger keys and ties (high half) of every round and warp, in position order
 #pragma unroll
-    for (int r = 0; r < R; ++r) {   // (all R: the scan reads every entry)
-      const uint32_t gt = __ballot_sync(0xffffffffu, keys[r] > thr);
-      const uint32_t eq = __ballot_sync(0xffffffffu, keys[r] == thr);
-      if (lane == 0) sh.hist[r * 32 + warp] = __popc(gt) | (__popc(eq) << 16);
+    for (int r = 0; r < R; ++r) {
+      uint32_t c = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        c += __popc(__ballot_sync(0xffffffffu, keys[r][e] > thr)) |
+             __popc(__ballot_sync(0xffffffffu, keys[r][e] == thr)) << 16;
+      if (lane == 0) sh.hist[r * 32 + warp] = c;
     }
     __syncthreads();
     const uint32_t c = (int)threadIdx.x < R * 32 ? sh.hist[threadIdx.x] : 0u;
@@ -1000,36 +1060,61 @@ __global__ void __launch_bounds__(kSelThr)
     }
     if (lane == 31) sh.warp_sum[warp] = inc;
     __syncthreads();
-    uint32_t base = 0;
-    for (int v = 0; v < warp; ++v) base += sh.warp_sum[v];
-    if ((int)threadIdx.x < R * 32) sh.hist[threadIdx.x] = base + inc - c;
-    __syncthreads();
-    // (the weights once more, eight in flight: a key does not give back NaN and -0)
+    uint32_t sum = 0;
 #pragma unroll
-    for (int r0 = 0; r0 < R; r0 += 8) {
+    for (int v = 0; v < R; ++v) sum += v < warp ? sh.warp_sum[v] : 0u;
+    if ((int)threadIdx.x < R * 32) sh.hist[threadIdx.x] = sum + inc - c;
+    if ((int)threadIdx.x == R * 32 - 1) sh.total = sum + inc;
+    uint32_t gt0 = 0, eq0 = 0;   // of the blocks before
+    if constexpr (C > 1) {
+      team_sync();
+      uint32_t t[C];
+#pragma unroll
+      for (int v = 0; v < C; ++v) t[v] = team_read(&sh.total, v);
+#pragma unroll
+      for (int v = 0; v < C; ++v)
+        if (v < rank) {
+          gt0 += t[v] & 0xffffu;
+          eq0 += t[v] >> 16;
+        }
+    } else {
+      __syncthreads();
+    }
+    // (the weights once more, of threads that keep any: a key does not give back NaN
+    // and -0)
+#pragma unroll
+    for (int r0 = 0; r0 < R; r0 += 2) {
       if (r0 >= rounds) break;
-      uint32_t raw[8];
+      uint32_t raw[2][4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (r0 + e < R)
-          raw[e] = load_once(w + min((r0 + e) * kSelThr + (int)threadIdx.x, n - 1));
+      for (int u = 0; u < 2; ++u) {
+        if (r0 + u >= R) break;
+        const uint32_t* k = keys[r0 + u];
+        const bool any = max(max(k[0], k[1]), max(k[2], k[3])) >= thr;
+        load_weights(w, x0 + (r0 + u) * kSelRound, any ? n : 0, wide, raw[u]);
+      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int r = r0 + e;
-        if (r >= R) break;
-        const uint32_t before = sh.hist[r * 32 + warp];
-        emit(r * kSelThr + threadIdx.x, keys[r], before & 0xffffu, before >> 16,
-             __uint_as_float(raw[e]));
+      for (int u = 0; u < 2; ++u) {
+        if (r0 + u >= R) break;
+        const uint32_t before = sh.hist[(r0 + u) * 32 + warp];
+        emit(x0 + (r0 + u) * kSelRound, keys[r0 + u], raw[u], gt0 + (before & 0xffffu),
+             eq0 + (before >> 16));
       }
     }
+    if constexpr (C > 1) team_sync();   // no block leaves before its total is read
   } else {
-    const int per = ((n + 31) / 32 + 31) / 32 * 32;   // positions of a warp
-    const int x0 = min(n, warp * per), x1 = min(n, x0 + per);
+    const int per = ((n + 31) / 32 + 127) / 128 * 128;   // positions of a warp
+    const int w0 = (int)min((long long)n, (long long)warp * per), w1 = min(n, w0 + per);
     uint32_t gt = 0, eq = 0;
-    for (int x = x0 + lane; x < x1; x += 32) {
-      const uint32_t k = key_of(x);
-      gt += k > thr;
-      eq += k == thr;
+    for (int x = w0 + 4 * lane; x < w1; x += 128) {
+      uint32_t v[4];
+      load_weights(w, x, w1, wide, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t k = x + e < w1 ? key_of(x + e, v[e]) : 0u;
+        gt += k > thr;
+        eq += k == thr;
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -1046,11 +1131,19 @@ __global__ void __launch_bounds__(kSelThr)
       gt += sh.hist[v];
       eq += sh.hist[32 + v];
     }
-    for (int x = x0; x < x1; x += 32) {
-      const uint32_t k = x + lane < x1 ? key_of(x + lane) : 0u;
-      emit(x + lane, k, gt, eq, w[min(x + lane, n - 1)]);
-      gt += __popc(__ballot_sync(0xffffffffu, k > thr));
-      eq += __popc(__ballot_sync(0xffffffffu, k == thr));
+    for (int x = w0 + 4 * lane; x - 4 * lane < w1; x += 128) {
+      uint32_t v[4], k[4];
+      load_weights(w, x, w1, wide, v);
+      uint32_t c = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k[e] = x + e < w1 ? key_of(x + e, v[e]) : 0u;
+      emit(x, k, v, gt, eq);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        c += __popc(__ballot_sync(0xffffffffu, k[e] > thr)) |
+             __popc(__ballot_sync(0xffffffffu, k[e] == thr)) << 16;
+      gt += c & 0xffffu;
+      eq += c >> 16;
     }
   }
 }
@@ -1215,25 +1308,36 @@ cudaError_t cache_evict(const CacheParams& p, int dtype, cudaStream_t st) {
   int* kept = p.kept ? p.kept : (int*)p.ws;
   const long long bk = (long long)p.B * p.K;
   if (bk > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  // registers for the positions a sequence can have; beyond 32768 the form without
-  if (p.max_len <= 4 * kSelThr)
-    evict_select_kernel<4><<<(unsigned)bk, kSelThr, 0, st>>>(p, kept);
-  else if (p.max_len <= kSelRegs * kSelThr)
-    evict_select_kernel<kSelRegs><<<(unsigned)bk, kSelThr, 0, st>>>(p, kept);
+  // Registers for the positions a sequence can have. Four blocks share a (b, kv head)
+  // where one each would leave SMs idle (8 x 32768 weights: 19 us for the call, 29 with
+  // one block each; 64 x 32768: 75 and 72), and where one could not hold the positions,
+  // as long as that is two rounds of the card at most (2 x 131072: 32 us, 124 without
+  // registers; 114 x 65504: 77 and 68).
+  if (bk * 4 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)bk, grid4 = (unsigned)(4 * bk);
+  if (p.max_len <= kSelRound)
+    evict_select_kernel<1, 1><<<grid, kSelThr, 0, st>>>(p, kept);
+  else if (p.max_len <= 8 * kSelRound && bk * 4 <= kSeqSms)
+    evict_select_kernel<2, 4><<<grid4, kSelThr, 0, st>>>(p, kept);
+  else if (p.max_len <= 8 * kSelRound)
+    evict_select_kernel<8, 1><<<grid, kSelThr, 0, st>>>(p, kept);
+  else if (p.max_len <= 32 * kSelRound && bk * 4 <= 2 * kSeqSms)
+    evict_select_kernel<8, 4><<<grid4, kSelThr, 0, st>>>(p, kept);
   else
-    evict_select_kernel<0><<<(unsigned)bk, kSelThr, 0, st>>>(p, kept);
+    evict_select_kernel<0, 1><<<grid, kSelThr, 0, st>>>(p, kept);
   note_launch();
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int cpr = p.hd / (dtype == SWIN_DTYPE_BF16 ? 8 : 4);
   const long long per = 256 * kCopy;
-  const long long blocks = ((long long)p.budget * cpr + per - 1) / per, grid = blocks * bk;
-  if ((long long)p.budget * cpr > 0x7fffff00LL || grid > 0x7fffffffLL)
+  const long long blocks = ((long long)p.budget * cpr + per - 1) / per;
+  if ((long long)p.budget * cpr > 0x7fffff00LL || blocks * bk > 0x7fffffffLL)
     return cudaErrorInvalidConfiguration;
+  const dim3 all((unsigned)(blocks * bk));
   return dtype == SWIN_DTYPE_BF16
-             ? launch_dependent(evict_copy_kernel<__nv_bfloat16>, dim3((unsigned)grid), 256, 0, st,
-                                p, (const int*)kept, (int)blocks)
-             : launch_dependent(evict_copy_kernel<float>, dim3((unsigned)grid), 256, 0, st, p,
+             ? launch_dependent(evict_copy_kernel<__nv_bfloat16>, all, 256, 0, st, p,
+                                (const int*)kept, (int)blocks)
+             : launch_dependent(evict_copy_kernel<float>, all, 256, 0, st, p,
                                 (const int*)kept, (int)blocks);
 }
 

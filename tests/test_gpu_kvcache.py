@@ -268,6 +268,13 @@ EVICT = [
     (2, 64, 64, 40, [2500, 2560], 4, 100, 2000),
     (1, 8, 16, 7, [100], 1, 0, 1),
     (1, 64, 16, 4000, [60000], 4, 64, 5000),          # more weights than shared memory holds
+    # four blocks to a sequence; rows of weights that start on no 16 bytes; many key
+    # heads; four blocks that are full; more positions than registers hold
+    (2, 8, 16, 600, [9600, 9001, 4097, 333, 0], 4, 100, 700),
+    (2, 16, 3, 3001, [9003, 8192, 4096], 3, 7, 300),
+    (8, 8, 16, 300, [4800, 4100, 1025, 1, 4799, 3000, 2049, 0, 500, 4400], 3, 10, 300),
+    (1, 8, 64, 2048, [131072], 4, 64, 5000),
+    (1, 8, 7, 19201, [134407], 4, 64, 700),
 ]
 
 
