@@ -27,9 +27,9 @@
 // Bound: per 128 x 128 tile of a head the tensor pipe needs 8 hd cycles (S and
 // O at 8192 FLOP per cycle and SM) and the exp unit 1024 (16 per cycle), so
 // head_dim 128 is bound by both alike, head_dim 64 by the exp unit. Measured: 437 us
-// for the first case above (1100 TFLOP/s), 44 us for the second. The tensor pipe is
-// then busy for two thirds of the time, counting the half more that S with N = 64
-// costs (both operands come from shared memory), the exp unit for half: a step
+// for the first case above (1100 TFLOP/s), 44 us for the second. The tensor cores are
+// then busy for 71% of the time, with what S costs because N = 64 (both operands come
+// from shared memory; the products themselves are 52%), the exp unit for 55%: a step
 // goes through two products, the softmax and four barriers, each waiting for the
 // one before, and TMEM has no room for more steps in flight. On the exp unit's
 // side there is nothing to gain: a polynomial on the FMA pipe for a quarter to all
