@@ -29,8 +29,8 @@
 // at 1.5 times the cost of N = 128, and one or two gradient products), the exp
 // unit and the softmax warps' latencies at 64. Measured: 8192 causal tokens, 8
 // heads x 128 (2 key heads), 476 us for the whole backward, 208 us of them the
-// query side (tensor pipe active 52% of the time, 65% with what N = 64 loses) and
-// 298 us the key side (47%) when profiled; two ragged sequences of 4096, 16 heads
+// query side (tensor cores busy 73% of the time, 52% without what N = 64 loses) and
+// 294 us the key side (64% and 47%) when profiled; two ragged sequences of 4096, 16 heads
 // x 64, window 512: 135 us (58 and 73 when profiled).
 #include "seq_tc.cuh"
 
