@@ -31,7 +31,7 @@
 // heads x 128 (2 key heads), 476 us for the whole backward, 208 us of them the
 // query side (tensor cores busy 73% of the time, 52% without what N = 64 loses) and
 // 294 us the key side (64% and 47%) when profiled; two ragged sequences of 4096, 16 heads
-// x 64, window 512: 135 us (58 and 73 when profiled).
+// x 64, window 512: 132 us (58 and 74 when profiled).
 #include "seq_tc.cuh"
 
 namespace swin {
@@ -154,7 +154,9 @@ __device__ __forceinline__ bool store_grad(uint32_t col, float mul, bool keep, v
   __syncwarp();
 #pragma unroll
   for (int c = 0; c < NC; c += 32) tmem_ld32(col + c, o + c);
-  tmem_wait_ld();
+  tmem_wait_ld_regs(o);
+#pragma unroll
+  for (int c = 32; c < NC; c += 32) reg_fence32(o + c);
   if (empty) {
     tc_fence_before();
     mbar_arrive(empty);

@@ -480,7 +480,8 @@ __global__ void __launch_bounds__(kSeqThreads, 1)
       for (int c = 0; c < HD; c += 64) {
         float o[64];
         tmem_load_cols<64>(o_col + c, o);
-        tmem_wait_ld();
+        tmem_wait_ld_regs(o);
+        reg_fence32(o + 32);
         if (c + 64 >= HD) {
           tc_fence_before();
           mbar_arrive(&o_empty[w]);
